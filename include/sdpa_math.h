@@ -52,7 +52,8 @@ typedef enum {
     SDPA_F32 = 0,
     SDPA_F16 = 1,
     SDPA_BF16 = 2,
-    SDPA_BOOL = 3 /* one byte per element, 0 = False */
+    SDPA_BOOL = 3, /* one byte per element, 0 = False */
+    SDPA_E4M3 = 4  /* 8-bit cache codes: 4 exponent bits, 3 mantissa bits, no infinities */
 } sdpa_dtype_t;
 
 /*

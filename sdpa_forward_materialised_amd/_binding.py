@@ -19,7 +19,7 @@ import torch
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libsdpa_math.so")
 
-SDPA_F32, SDPA_F16, SDPA_BF16, SDPA_BOOL = 0, 1, 2, 3
+SDPA_F32, SDPA_F16, SDPA_BF16, SDPA_BOOL, SDPA_E4M3 = 0, 1, 2, 3, 4
 PATH_AUTO, PATH_FUSED, PATH_TWOPASS = 0, 1, 2
 PATHS = {"auto": PATH_AUTO, "fused": PATH_FUSED, "twopass": PATH_TWOPASS}
 PATH_FUSED_WIDE = 3  # reported by sdpa_math_plan: the fused path on its wide kernel
@@ -29,12 +29,14 @@ KERNEL_NAMES = {PATH_FUSED: "sdpa_fused_kernel", PATH_FUSED_WIDE: "sdpa_fused_wi
 CAUSAL_ALIGNMENTS = {"top_left": 1, "bottom_right": 2}  # the C ABI's is_causal codes
 
 _DTYPES = {torch.float32: SDPA_F32, torch.float16: SDPA_F16, torch.bfloat16: SDPA_BF16,
-           torch.bool: SDPA_BOOL}
+           torch.bool: SDPA_BOOL, torch.float8_e4m3fn: SDPA_E4M3}
 
 EXPORTS = ("sdpa_math_fwd", "sdpa_math_fwd_path", "sdpa_math_fwd_ws", "sdpa_math_workspace_bytes",
            "sdpa_math_fwd_noalloc", "sdpa_math_fwd_dropout", "sdpa_math_fwd_varlen", "sdpa_math_bwd", "sdpa_math_bwd_workspace_bytes", "sdpa_math_plan",
            "sdpa_math_last_error",
-           "sdpa_math_version", "sdpa_probe_fill", "sdpa_probe_copy")
+           "sdpa_math_version", "sdpa_probe_fill", "sdpa_probe_copy",
+           "sdpa_prompt_fwd", "sdpa_key_weights", "sdpa_key_weights_workspace_bytes", "sdpa_cache_append",
+           "sdpa_cache_attention", "sdpa_cache_attention_workspace_bytes", "sdpa_cache_evict")
 
 
 class SdpaTensor(ctypes.Structure):
@@ -90,6 +92,18 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.sdpa_math_plan.restype = ctypes.c_int
     lib.sdpa_math_plan.argtypes = [T, T, T, T, ctypes.c_int, ctypes.c_int, ctypes.POINTER(ctypes.c_int32),
                                    ctypes.POINTER(ctypes.c_int64), ctypes.POINTER(ctypes.c_int64)]
+    # serving operators: pointers, 64-bit counts, ints
+    P, N, I, F, Z = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+    for name, args in (
+            ("sdpa_prompt_fwd", [T, T, T, P, P, N, N, N, I, F, I, T, T, P]),
+            ("sdpa_key_weights", [T, T, T, P, P, N, N, N, I, F, I, T, P, Z, P]),
+            ("sdpa_key_weights_workspace_bytes", [T, T, N, N, N, I, ctypes.POINTER(Z)]),
+            ("sdpa_cache_append", [T, T, T, P, N, N, N, P, P, N, P]),
+            ("sdpa_cache_attention", [T, T, P, N, N, N, P, P, N, N, I, F, I, T, T, T, T, P, Z, P]),
+            ("sdpa_cache_attention_workspace_bytes", [T, T, N, N, N, N, I, I, ctypes.POINTER(Z)]),
+            ("sdpa_cache_evict", [T, P, N, N, N, P, T, T, N, N, P, N, N, P, P, P])):
+        fn = getattr(lib, name)
+        fn.restype, fn.argtypes = ctypes.c_int, args
     lib.sdpa_math_last_error.restype = ctypes.c_char_p
     lib.sdpa_math_last_error.argtypes = []
     lib.sdpa_math_version.restype = ctypes.c_int

@@ -1,0 +1,257 @@
+"""Binding of the serving operators (``include/sdpa_serve.h``): attention over
+packed prompts without the probability map, the attention weight each key
+received, and the paged 8-bit cache.
+
+Argument marshalling only, like the rest of the binding: workspaces and default
+outputs come from torch's caching allocator, the launch goes to torch's current
+stream on the tensors' device, and nothing here synchronises or reads device
+data. A tensor that was produced on another stream has to be ordered before the
+call by the caller, as for any torch operator.
+"""
+
+from __future__ import annotations
+
+import ctypes
+import math
+from typing import Optional, Tuple
+
+import torch
+
+from ._binding import _causal_code, _check_devices, _current_stream, _desc, _raise, load_library
+
+_BYTES = {}  # workspace bytes per call signature (shapes and flags)
+
+
+class PagedCache:
+    """A pool of pages of an 8-bit key/value cache.
+
+    ``k`` [n_pages, Hkv, page, D] and ``v`` [n_pages, Hkv, D, page] (the tokens
+    of a page innermost) hold float8_e4m3fn codes; ``k_scale`` and ``v_scale``
+    [n_pages, Hkv] (float32) the power of two that a page's and head's codes are
+    multiplied with. The tensors must keep their storage while the object lives.
+    """
+
+    __slots__ = ("k", "v", "k_scale", "v_scale", "_bytes", "_device")
+
+    def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor):
+        for name, t, nd in (("k", k, 4), ("v", v, 4), ("k_scale", k_scale, 2), ("v_scale", v_scale, 2)):
+            if t.dim() != nd:
+                raise ValueError(f"cache {name} must have {nd} dims, got {t.dim()}")
+            if t.device != k.device:
+                raise ValueError(f"cache tensors on different devices ({k.device} and {t.device})")
+        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self._bytes = _desc(k, 4) + _desc(v, 4) + _desc(k_scale, 2) + _desc(v_scale, 2)
+        self._device = k.device
+
+    @property
+    def page_tokens(self) -> int:
+        return self.k.shape[2]
+
+
+def new_cache(n_pages: int, heads: int, head_dim: int, page_tokens: int = 64, device="cuda") -> PagedCache:
+    """A pool of zeroed pages."""
+    return PagedCache(torch.zeros((n_pages, heads, page_tokens, head_dim), dtype=torch.float8_e4m3fn, device=device),
+                      torch.zeros((n_pages, heads, head_dim, page_tokens), dtype=torch.float8_e4m3fn, device=device),
+                      torch.zeros((n_pages, heads), dtype=torch.float32, device=device),
+                      torch.zeros((n_pages, heads), dtype=torch.float32, device=device))
+
+
+def _offsets(name: str, t: torch.Tensor, n: Optional[int] = None) -> None:
+    if t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous 1-D int32 tensor")
+    if n is not None and t.numel() != n:
+        raise ValueError(f"{name} holds {t.numel()} entries, expected {n}")
+
+
+def _table(name: str, t: torch.Tensor, n_seqs: int) -> None:
+    if t.dtype != torch.int32 or t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be a 2-D int32 tensor, contiguous in its last dim")
+    if t.shape[0] != n_seqs:
+        raise ValueError(f"{name} has {t.shape[0]} rows, expected {n_seqs}")
+
+
+def _packed(name: str, t: torch.Tensor) -> None:
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be 3-D [T, H, D]")
+
+
+def _cu_pair(cu_q: torch.Tensor, cu_kv: torch.Tensor) -> int:
+    _offsets("cu_seqlens_q", cu_q)
+    _offsets("cu_seqlens_kv", cu_kv)
+    if cu_q.numel() != cu_kv.numel() or cu_q.numel() < 1:
+        raise ValueError("cu_seqlens_q and cu_seqlens_kv must hold n_seqs + 1 offsets each")
+    return cu_q.numel() - 1
+
+
+def _scale(scale: Optional[float], D: int) -> float:
+    if scale is not None:
+        return float(scale)
+    return 1.0 / math.sqrt(D) if D > 0 else 1.0
+
+
+def _call(lib, fn, dev: torch.device, *args) -> None:
+    """``fn(*args, stream)`` on the tensors' device (made current only when it is not)."""
+    if dev.index == torch.cuda.current_device():
+        rc = fn(*args, _current_stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            rc = fn(*args, _current_stream(dev))
+    if rc != 0:
+        _raise(rc, lib)
+
+
+def _workspace(lib, fn, dev: torch.device, sig, *args):
+    """(workspace or None, its bytes) of a call with this signature."""
+    n = _BYTES.get(sig)
+    if n is None:
+        c = ctypes.c_size_t(0)
+        rc = fn(*args, ctypes.byref(c))
+        if rc != 0:
+            _raise(rc, lib)
+        if len(_BYTES) >= 4096:  # many distinct shapes: start over rather than grow
+            _BYTES.clear()
+        n = _BYTES[sig] = c.value
+    return (torch.empty(n, dtype=torch.uint8, device=dev), n) if n > 0 else (None, 0)
+
+
+def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens_q: torch.Tensor,
+                     cu_seqlens_kv: torch.Tensor, max_seqlen_q: int, max_seqlen_kv: int, is_causal: bool = True,
+                     scale: Optional[float] = None, enable_gqa: bool = False, causal_alignment: str = "top_left",
+                     out: Optional[Tuple[torch.Tensor, torch.Tensor]] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """``sdpa_prompt_fwd``: (O [Tq, Hq, D], LSE [Tq, Hq] float32) of packed
+    sequences q [Tq, Hq, D], k/v [Tkv, Hkv, D], without the probability map.
+    Arguments as ``fwd_varlen``, except that it is causal by default; ``out``
+    may pass (O, LSE). Tokens of no sequence are not written."""
+    lib = load_library()
+    dev = _check_devices(q, k, v, cu_seqlens_q, cu_seqlens_kv)
+    n = _cu_pair(cu_seqlens_q, cu_seqlens_kv)
+    causal = _causal_code(is_causal, causal_alignment)
+    _packed("q", q), _packed("k", k), _packed("v", v)
+    if out is None:
+        O = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        L = torch.empty(q.shape[:2], dtype=torch.float32, device=dev)
+    else:
+        O, L = out
+        _check_devices(q, O, L)
+    _call(lib, lib.sdpa_prompt_fwd, dev, _desc(q, 3), _desc(k, 3), _desc(v, 3), cu_seqlens_q.data_ptr(),
+          cu_seqlens_kv.data_ptr(), n, int(max_seqlen_q), int(max_seqlen_kv), causal, _scale(scale, q.shape[2]),
+          int(bool(enable_gqa)), _desc(O, 3), _desc(L, 2))
+    return O, L
+
+
+def key_weights(q: torch.Tensor, k: torch.Tensor, lse: torch.Tensor, cu_seqlens_q: torch.Tensor,
+                cu_seqlens_kv: torch.Tensor, max_seqlen_q: int, max_seqlen_kv: int, is_causal: bool = True,
+                scale: Optional[float] = None, enable_gqa: bool = False, causal_alignment: str = "top_left",
+                out: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """``sdpa_key_weights``: the attention weight every key received, summed
+    over its sequence's rows and its key head's query heads, float32
+    [n_seqs, Hkv, max_seqlen_kv] with zeros past each sequence's keys. ``lse``
+    is that of ``prompt_attention`` (or ``fwd_varlen``) on the same arguments;
+    ``out`` may pass the result's tensor (last dim contiguous: a slice of the
+    weights that ``cache_attention`` adds to, for instance)."""
+    lib = load_library()
+    dev = _check_devices(q, k, lse, cu_seqlens_q, cu_seqlens_kv)
+    n = _cu_pair(cu_seqlens_q, cu_seqlens_kv)
+    causal = _causal_code(is_causal, causal_alignment)
+    _packed("q", q), _packed("k", k)
+    max_q, max_kv, gqa = int(max_seqlen_q), int(max_seqlen_kv), int(bool(enable_gqa))
+    if out is None:
+        out = torch.empty((n, k.shape[1], max(0, max_kv)), dtype=torch.float32, device=dev)
+    else:
+        _check_devices(q, out)
+    dq, dk = _desc(q, 3), _desc(k, 3)
+    ws, nbytes = _workspace(lib, lib.sdpa_key_weights_workspace_bytes, dev,
+                            ("weights", q.shape, k.shape, q.dtype, n, max_q, max_kv), dq, dk, n, max_q, max_kv, 1)
+    _call(lib, lib.sdpa_key_weights, dev, dq, dk, _desc(lse, 2), cu_seqlens_q.data_ptr(), cu_seqlens_kv.data_ptr(), n,
+          max_q, max_kv, causal, _scale(scale, q.shape[2]), gqa, _desc(out, 3), None if ws is None else ws.data_ptr(),
+          nbytes)
+    return out
+
+
+def cache_append(cache: PagedCache, k: torch.Tensor, v: torch.Tensor, page_table: torch.Tensor, kv_lens: torch.Tensor,
+                 cu_seqlens: torch.Tensor, max_new: int) -> None:
+    """``sdpa_cache_append``: write new tokens k/v [T, Hkv, D] (sequence b's are
+    cu_seqlens[b] .. cu_seqlens[b + 1], at most ``max_new``) behind the
+    ``kv_lens`` [n_seqs] tokens that the sequences hold. ``page_table``
+    [n_seqs, max_pages] lists their pages. ``kv_lens`` is not changed."""
+    lib = load_library()
+    dev = _check_devices(cache.k, k, v, page_table, kv_lens, cu_seqlens)
+    n = kv_lens.shape[0] if kv_lens.dim() == 1 else -1
+    _offsets("kv_lens", kv_lens)
+    _offsets("cu_seqlens", cu_seqlens, n + 1)
+    _table("page_table", page_table, n)
+    _packed("k", k), _packed("v", v)
+    _call(lib, lib.sdpa_cache_append, dev, cache._bytes, _desc(k, 3), _desc(v, 3), page_table.data_ptr(), n,
+          page_table.shape[1], page_table.stride(0), kv_lens.data_ptr(), cu_seqlens.data_ptr(), int(max_new))
+
+
+def cache_attention(q: torch.Tensor, cache: PagedCache, page_table: torch.Tensor, kv_lens: torch.Tensor,
+                    cu_seqlens_q: torch.Tensor, max_seqlen_q: int, max_kv: Optional[int] = None,
+                    is_causal: bool = True, scale: Optional[float] = None, enable_gqa: bool = False,
+                    weights: Optional[torch.Tensor] = None, weights_out: Optional[torch.Tensor] = None,
+                    out: Optional[Tuple[torch.Tensor, torch.Tensor]] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """``sdpa_cache_attention``: (O [T, Hq, D], LSE [T, Hq] float32) of the last
+    tokens of every sequence, q [T, Hq, D] packed by ``cu_seqlens_q``, over its
+    ``kv_lens`` cached tokens (these tokens' own keys among them). ``max_kv``
+    bounds the lengths (default: the page table's capacity). With ``weights``
+    [n_seqs, Hkv, W] (float32), every key's probability, summed over its key
+    head's query heads and the new tokens, is added to them, in place or into
+    ``weights_out``."""
+    lib = load_library()
+    dev = _check_devices(q, cache.k, page_table, kv_lens, cu_seqlens_q, weights, weights_out)
+    n = kv_lens.shape[0] if kv_lens.dim() == 1 else -1
+    _offsets("kv_lens", kv_lens)
+    _offsets("cu_seqlens_q", cu_seqlens_q, n + 1)
+    _table("page_table", page_table, n)
+    _packed("q", q)
+    if weights is None and weights_out is not None:
+        raise ValueError("weights_out needs weights")
+    if weights is not None and weights_out is None:
+        weights_out = weights
+    max_pages, max_q, gather = page_table.shape[1], int(max_seqlen_q), int(weights is not None)
+    max_kv = max_pages * cache.k.shape[2] if max_kv is None else int(max_kv)
+    if out is None:
+        O = torch.empty(q.shape, dtype=q.dtype, device=dev)
+        L = torch.empty(q.shape[:2], dtype=torch.float32, device=dev)
+    else:
+        O, L = out
+        _check_devices(q, O, L)
+    dq, gqa = _desc(q, 3), int(bool(enable_gqa))
+    ws, nbytes = _workspace(lib, lib.sdpa_cache_attention_workspace_bytes, dev,
+                            ("cache", q.shape, cache.k.shape, n, max_pages, max_q, max_kv, gqa, gather), dq,
+                            cache._bytes, n, max_pages, max_q, max_kv, gqa, gather)
+    _call(lib, lib.sdpa_cache_attention, dev, dq, cache._bytes, page_table.data_ptr(), n, max_pages,
+          page_table.stride(0), kv_lens.data_ptr(), cu_seqlens_q.data_ptr(), max_q, max_kv, int(bool(is_causal)),
+          _scale(scale, q.shape[2]), gqa, None if weights is None else _desc(weights, 3),
+          None if weights is None else _desc(weights_out, 3), _desc(O, 3), _desc(L, 2),
+          None if ws is None else ws.data_ptr(), nbytes)
+    return O, L
+
+
+def cache_evict(cache: PagedCache, page_table: torch.Tensor, kv_lens: torch.Tensor, weights: torch.Tensor, budget: int,
+                recent: int, to_table: torch.Tensor, weights_out: Optional[torch.Tensor] = None
+                ) -> Tuple[torch.Tensor, torch.Tensor]:
+    """``sdpa_cache_evict``: keep at most ``budget`` tokens of every sequence and
+    key head, its ``recent`` last ones and those with the largest ``weights``
+    [n_seqs, Hkv, W]; they move, in order, to the pages of ``to_table``
+    [n_seqs, to_pages], which must hold no token of a sequence in this call.
+    The kept tokens' weights (zeros behind them) replace ``weights`` or go to
+    ``weights_out``. Returns (the positions kept, int32 [n_seqs, Hkv, budget]
+    with -1 behind them; the new lengths, int32 [n_seqs])."""
+    lib = load_library()
+    dev = _check_devices(cache.k, page_table, kv_lens, weights, weights_out, to_table)
+    n = kv_lens.shape[0] if kv_lens.dim() == 1 else -1
+    _offsets("kv_lens", kv_lens)
+    _table("page_table", page_table, n)
+    _table("to_table", to_table, n)
+    budget = int(budget)
+    if budget < 1:
+        raise ValueError("budget must be at least 1")
+    if weights_out is None:
+        weights_out = weights
+    kept = torch.empty((n, cache.k.shape[1], budget), dtype=torch.int32, device=dev)
+    lens = torch.empty((n,), dtype=torch.int32, device=dev)
+    _call(lib, lib.sdpa_cache_evict, dev, cache._bytes, page_table.data_ptr(), n, page_table.shape[1],
+          page_table.stride(0), kv_lens.data_ptr(), _desc(weights, 3), _desc(weights_out, 3), budget, int(recent),
+          to_table.data_ptr(), to_table.shape[1], to_table.stride(0), kept.data_ptr(), lens.data_ptr())
+    return kept, lens

@@ -6,66 +6,16 @@
 
 #include <algorithm>
 #include <cmath>
-#include <cstdarg>
-#include <cstdio>
 #include <cstdlib>
 #include <cstring>
-#include <string>
 
+#include "api_checks.h"
 #include "sdpa_internal.h"
 #include "sdpa_math.h"
 
+using namespace sdpa_api;
+
 namespace {
-
-thread_local std::string g_last_error;
-
-sdpa_status_t fail(sdpa_status_t st, const char* fmt, ...) {
-    char buf[512];
-    va_list ap;
-    va_start(ap, fmt);
-    vsnprintf(buf, sizeof buf, fmt, ap);
-    va_end(ap);
-    g_last_error = buf;
-    return st;
-}
-
-int64_t elt_size(int dtype) {
-    switch (dtype) {
-        case SDPA_F32: return 4;
-        case SDPA_F16:
-        case SDPA_BF16: return 2;
-        case SDPA_BOOL: return 1;
-        default: return 0;
-    }
-}
-
-const char* dtype_name(int dtype) {
-    switch (dtype) {
-        case SDPA_F32: return "f32";
-        case SDPA_F16: return "f16";
-        case SDPA_BF16: return "bf16";
-        case SDPA_BOOL: return "bool";
-        default: return "?";
-    }
-}
-
-int64_t numel(const sdpa_tensor_t* t) {
-    int64_t n = 1;
-    for (int d = 0; d < t->ndim; ++d) n *= t->sizes[d];
-    return n;
-}
-
-// Effective stride: a size-1 dim never advances, whatever stride it carries.
-int64_t eff_stride(const sdpa_tensor_t* t, int d) { return t->sizes[d] == 1 ? 0 : t->strides[d]; }
-
-// True when every row start (all dims but the last) is `align`-byte aligned.
-bool rows_aligned(const sdpa_tensor_t* t, int64_t align) {
-    const int64_t es = elt_size(t->dtype);
-    if (reinterpret_cast<uintptr_t>(t->data) % align) return false;
-    for (int d = 0; d + 1 < t->ndim; ++d)
-        if ((eff_stride(t, d) * es) % align) return false;
-    return true;
-}
 
 struct Shape {
     int64_t B, Hq, Hkv, Sq, Skv, D, Dv;
@@ -73,28 +23,6 @@ struct Shape {
     int mask_kind;
     bool mask_head_shared;  // no mask, or one that every query head shares (size 1 or stride 0)
 };
-
-sdpa_status_t check_tensor(const sdpa_tensor_t* t, const char* name, int ndim) {
-    if (!t) return fail(SDPA_ERR_INVALID_ARG, "%s is NULL", name);
-    if (t->ndim != ndim) return fail(SDPA_ERR_INVALID_ARG, "%s must have %d dims, got %d", name, ndim, t->ndim);
-    for (int d = 0; d < ndim; ++d)
-        if (t->sizes[d] < 0) return fail(SDPA_ERR_INVALID_ARG, "%s has a negative size", name);
-    if (elt_size(t->dtype) == 0) return fail(SDPA_ERR_INVALID_ARG, "%s has an unknown dtype %d", name, t->dtype);
-    if (numel(t) > 0 && t->data == nullptr) return fail(SDPA_ERR_INVALID_ARG, "%s has no data pointer", name);
-    if (numel(t) > 0 && t->sizes[ndim - 1] > 1 && t->strides[ndim - 1] != 1)
-        return fail(SDPA_ERR_UNSUPPORTED, "%s must be contiguous in its last dim (stride %lld)", name,
-                    (long long)t->strides[ndim - 1]);
-    return SDPA_OK;
-}
-
-sdpa_status_t check_dims(const sdpa_tensor_t* t, const char* name, const int64_t* want, int ndim) {
-    for (int d = 0; d < ndim; ++d)
-        if (t->sizes[d] != want[d]) {
-            return fail(SDPA_ERR_INVALID_ARG, "%s dim %d is %lld, expected %lld", name, d, (long long)t->sizes[d],
-                        (long long)want[d]);
-        }
-    return SDPA_OK;
-}
 
 sdpa_status_t validate_inputs(const sdpa_tensor_t* q, const sdpa_tensor_t* k, const sdpa_tensor_t* v,
                               const sdpa_tensor_t* mask, int is_causal, int enable_gqa, Shape* sh) {
@@ -182,8 +110,6 @@ sdpa_status_t validate_outputs(const Shape& sh, const sdpa_tensor_t* out, const 
         return st;
     return SDPA_OK;
 }
-
-int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Causal diagonal offset: key j is removed for query i when j > i + offset
 // (is_causal 1: top-left, offset 0; 2: bottom-right, the alignment of a query
@@ -781,12 +707,6 @@ sdpa_status_t run(const sdpa_tensor_t* q, const sdpa_tensor_t* k, const sdpa_ten
                      plan.n_splits, (long long)plan.grid,
                      (long long)plan.tiles_per_bh, (long long)plan.tiles_64);
     return SDPA_OK;
-}
-
-// Byte extent of one (batch, head) slice: `rows` rows of `cols` elements at
-// a row pitch of `pitch` elements (0 rows: 0).
-int64_t slice_extent(int64_t rows, int64_t pitch, int64_t cols, int64_t es) {
-    return rows > 0 && cols > 0 ? ((rows - 1) * pitch + cols) * es : 0;
 }
 
 // Query ranges of the combined key-side backward launch (causal calls):
