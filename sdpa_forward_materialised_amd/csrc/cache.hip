@@ -555,92 +555,185 @@ int launch_cache_attention(int dtype, const CacheArgs& a, void* stream) {
 // --------------------------------------------------------------------- eviction
 //
 // sdpa_cache_select_kernel: one workgroup per (sequence, key head) finds the
-// tokens to keep. Weights become integers of the same order (NaN highest);
-// three passes of a radix histogram (11, 11 and 10 bits) find the value of
-// the last token kept; then each wave counts, and after a scan over the waves
-// emits, the kept tokens of its stretch of the sequence in order, of the tied
-// ones the first.
+// tokens to keep. The weights of the candidates (the tokens before the recent
+// ones) become integers of the same order (NaN highest), kept in LDS where
+// they fit; a radix histogram of 11, 11 and 10 bits, the first one taken while
+// the weights are loaded, the last over a list of the tokens that share the
+// bits found so far, gives the value of the last candidate kept. One more pass
+// marks the kept ones and those tied with the last, as bits of a word for
+// every 64 tokens, and after a scan over the waves' counts each wave emits its
+// kept tokens in order, of the tied ones the first. Counts are integers and
+// the list's order has no effect, so the atomics leave nothing to chance. One
+// CU's latencies bound it.
 __device__ __forceinline__ uint32_t order_key(float x) {
     const uint32_t u = __builtin_bit_cast(uint32_t, x);
-    if (x != x) return 0xffffffffu;
-    if (x == 0.0f) return 0x80000000u;
-    return u & 0x80000000u ? ~u : u | 0x80000000u;
+    const uint32_t k = u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);  // negative: all bits turn, else the sign
+    const uint32_t mag = u << 1;
+    return mag > 0xff000000u ? 0xffffffffu : mag == 0u ? 0x80000000u : k;  // NaN; -0 as 0
+}
+__device__ __forceinline__ float key_value(uint32_t k) {
+    if (k == 0xffffffffu) return __builtin_bit_cast(float, 0x7fc00000u);
+    return __builtin_bit_cast(float, k & 0x80000000u ? k ^ 0x80000000u : ~k);
 }
 
 constexpr int SELECT_THREADS = 1024;
+constexpr int SELECT_LIST = 1024;
 
+// CAP: candidates whose keys LDS holds, a multiple of 4096 (0: any number,
+// read again from memory).
+template <int CAP>
 __global__ __attribute__((amdgpu_flat_work_group_size(SELECT_THREADS, SELECT_THREADS)))
 void sdpa_cache_select_kernel(const CacheArgs a) {
-    constexpr int NT = SELECT_THREADS, NWV = NT / 64;
-    __shared__ int hist[2048];
+    constexpr int NT = SELECT_THREADS, NWV = NT / 64, NB = 2048;
+    constexpr int WORDS = CAP > 0 ? CAP / 64 : 1;
+    __shared__ __attribute__((aligned(16))) uint32_t keys[CAP > 0 ? CAP : 1];
+    __shared__ uint64_t kept_bits[WORDS], tied_bits[WORDS];
+    __shared__ int hist[NB];
+    __shared__ uint32_t list[SELECT_LIST];
     __shared__ int wsum[NWV], wtie[NWV];
-    __shared__ int pick_s, above_s;
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    __shared__ int pick_s, above_s, bin_s, list_n;
+    const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int h = blockIdx.x % a.Hkv, b = blockIdx.x / a.Hkv;
     const int len = (int)min((int64_t)held_tokens(a, b), (int64_t)a.w_cols);
     const int n = min(len, a.budget);
-    const int late = len - min(a.recent, n);  // tokens from here on are kept
-    int need = n - (len - late);              // of the tokens before
+    const int late = len - min(a.recent, n);  // tokens from here on are kept, those before are candidates
+    const int take = n - (len - late);        // candidates kept
     const float* w = a.w_in + b * a.wi_s[0] + h * a.wi_s[1];
+    float* wo = a.w_out + b * a.wo_s[0] + h * a.wo_s[1];
     int* kept = a.kept + ((int64_t)b * a.Hkv + h) * a.budget;
+    const bool some = take > 0 && take < late;
+    // a wave's stretch: `words` words of 64 tokens, a multiple of 4
+    const int words = ((late + 4 * NT - 1) / (4 * NT)) * 4;
+    const int t0 = wave * words * 64 + lane;
 
-    uint32_t pick = 0;   // the order key of the last token kept, found from the high bits down
-    const bool all = need == late;
-    if (!all && need > 0) {
+    auto clear = [&]() SDPA_INLINE {
+        for (int i = tid; i < NB; i += NT) hist[i] = 0;
+    };
+    // one more token in bin `bin` for every lane with `in` (all lanes call)
+    auto add = [&](int bin, bool in) SDPA_INLINE {
+        const uint64_t who = __builtin_amdgcn_ballot_w64(in);
+        if (who == 0) return;
+        const int first = __builtin_amdgcn_readlane(bin, __builtin_ctzll(who));
+        if (__builtin_amdgcn_ballot_w64(in && bin != first) == 0) {  // one bin (equal weights): one addition
+            if (lane == 0) atomicAdd(&hist[first], __popcll(who));
+        } else if (in) {
+            atomicAdd(&hist[bin], 1);
+        }
+    };
+    // keys of the words i .. i + 3 of this wave; no candidate has key 0
+    auto four = [&](int i, uint32_t* k) SDPA_INLINE {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int j = t0 + 64 * (i + e);
+            if constexpr (CAP > 0) k[e] = keys[j];
+            else k[e] = j < late ? order_key(w[j]) : 0u;
+        }
+    };
+    float recent[4];  // the first recent weights, in flight behind all that follows
+    if constexpr (CAP > 0) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) recent[e] = e * NT + tid < len - late ? w[late + e * NT + tid] : 0.0f;
+    }
+    clear();
+    if (tid == 0) list_n = 0;
+    __syncthreads();
+    for (int i = 0; i < words; i += 8) {  // every key, and the histogram of the highest bits
+        float x[8];
+        const int m = min(8, words - i);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const int j = t0 + 64 * (i + e);
+            x[e] = e < m && j < late ? w[j] : 0.0f;
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            if (e >= m) break;
+            const int j = t0 + 64 * (i + e);
+            const uint32_t k = j < late ? order_key(x[e]) : 0u;
+            if constexpr (CAP > 0) keys[j] = k;
+            if (some) add((int)(k >> 21), j < late);
+        }
+    }
+    // the largest `pick` that `take` candidates reach, and how many of those equal to it are kept
+    uint32_t pick = 0;
+    int need = take;
+    if (some) {
         uint32_t mask = 0;
-        const int shifts[3] = {21, 10, 0}, bits[3] = {11, 11, 10};
-#pragma unroll
         for (int pass = 0; pass < 3; ++pass) {
-            const int nb = 1 << bits[pass];
-            for (int i = tid; i < nb; i += NT) hist[i] = 0;
-            __syncthreads();
-            for (int j = tid; j < late; j += NT) {
-                const uint32_t u = order_key(w[j]);
-                if ((u & mask) == pick) atomicAdd(&hist[(u >> shifts[pass]) & (nb - 1)], 1);
-            }
-            __syncthreads();
-            // the highest bin that, with all above it, holds `need` tokens
-            if (wave == 0) {
-                int run = 0;
-                for (int base = nb - 64; base >= 0; base -= 64) {
-                    const int c = hist[base + 63 - lane];
-                    int x = c;  // sums over the lanes up to this one: bins from the top down
+            const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1024 : 2048;
+            const bool listed = pass == 2 && bin_s <= SELECT_LIST;  // bin_s: tokens that share the first 11 bits
+            if (pass > 0) {
+                clear();
+                __syncthreads();
+                if (listed) {
+                    for (int i = tid & ~63; i < list_n; i += NT) {
+                        const uint32_t k = i + lane < list_n ? list[i + lane] : 0u;
+                        add((int)(k >> shift) & (bins - 1), (k & mask) == pick);
+                    }
+                } else {
+                    const bool make = pass == 1 && bin_s <= SELECT_LIST;
+                    for (int i = 0; i < words; i += 4) {
+                        uint32_t k[4];
+                        four(i, k);
 #pragma unroll
-                    for (int k = 1; k < 64; k *= 2) {
-                        const int y = __shfl_up(x, k);
-                        if (lane >= k) x += y;
-                    }
-                    const uint64_t hit = __builtin_amdgcn_ballot_w64(run + x >= need);
-                    if (hit) {
-                        const int f = __builtin_ctzll(hit);
-                        if (lane == f) {
-                            pick_s = base + 63 - lane;
-                            above_s = run + x - c;
+                        for (int e = 0; e < 4; ++e) {
+                            const bool in = (k[e] & mask) == pick;
+                            add((int)(k[e] >> shift) & (bins - 1), in);
+                            if (make && in) list[atomicAdd(&list_n, 1)] = k[e];
                         }
-                        break;
                     }
-                    run += __shfl(x, 63);
                 }
             }
             __syncthreads();
-            pick |= (uint32_t)pick_s << shifts[pass];
-            mask |= (uint32_t)(nb - 1) << shifts[pass];
-            need -= above_s;
+            // the highest bin that, with all above it, holds `need` tokens:
+            // a wave sums 128 bins, from the top down over lanes and waves
+            const int top = NB - 1 - wave * 128 - 2 * lane;
+            const int c0 = hist[top], c1 = hist[top - 1];
+            int x = c0 + c1;
+#pragma unroll
+            for (int k = 1; k < 64; k *= 2) {
+                const int y = __shfl_up(x, k);
+                if (lane >= k) x += y;
+            }
+            if (lane == 63) wsum[wave] = x;
             __syncthreads();
+            int before = 0;
+            for (int i = 0; i < wave; ++i) before += wsum[i];
+            const int upto = before + x;  // tokens in the bins down to this lane's second
+            if (upto >= need && upto - c0 - c1 < need) {
+                const bool one = upto - c1 >= need;
+                pick_s = one ? top : top - 1;
+                above_s = one ? upto - c1 - c0 : upto - c1;
+                if (pass == 0) bin_s = one ? c0 : c1;
+            }
+            __syncthreads();
+            pick |= (uint32_t)pick_s << shift;
+            mask |= (uint32_t)(bins - 1) << shift;
+            need -= above_s;
         }
+    } else {
+        pick = take == 0 ? 0xffffffffu : 0u;  // none (ties count 0 below), or every candidate
+        need = 0;
+        __syncthreads();
     }
-    // need: how many tokens equal to `pick` are kept
-    const int per = ((len + NT - 1) / NT) * 64;  // a wave's stretch
-    const int w0 = min(len, wave * per), w1 = min(len, w0 + per);
-    const bool none = n - (len - late) == 0;
-    auto above = [&](int j, uint32_t u) SDPA_INLINE { return j >= late || (!none && (all || u > pick)); };
-    auto tied = [&](int j, uint32_t u) SDPA_INLINE { return j < late && !none && !all && u == pick; };
+    // mark and count
     int cnt = 0, tie = 0;
-    for (int j0 = w0; j0 < w1; j0 += 64) {
-        const int j = j0 + lane;
-        const uint32_t u = j < w1 ? order_key(w[j]) : 0u;
-        cnt += __popcll(__builtin_amdgcn_ballot_w64(j < w1 && above(j, u)));
-        tie += __popcll(__builtin_amdgcn_ballot_w64(j < w1 && tied(j, u)));
+    for (int i = 0; i < words; i += 4) {
+        uint32_t k[4];
+        four(i, k);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const uint64_t kb = __builtin_amdgcn_ballot_w64(k[e] > pick);
+            const uint64_t tb = __builtin_amdgcn_ballot_w64(k[e] == pick && pick != 0);
+            cnt += __popcll(kb);
+            tie += __popcll(tb);
+            if constexpr (CAP > 0) {
+                if (lane == 0) {
+                    kept_bits[wave * words + i + e] = kb;
+                    tied_bits[wave * words + i + e] = tb;
+                }
+            }
+        }
     }
     if (lane == 0) {
         wsum[wave] = cnt;
@@ -649,116 +742,234 @@ void sdpa_cache_select_kernel(const CacheArgs a) {
     __syncthreads();
     int at = 0, ties = 0;
     for (int i = 0; i < wave; ++i) {
-        const int before = min(ties + wtie[i], need) - min(ties, need);
-        at += wsum[i] + before;
+        at += wsum[i] + min(ties + wtie[i], need) - min(ties, need);
         ties += wtie[i];
     }
     const uint64_t below = (uint64_t(1) << lane) - 1;
-    for (int j0 = w0; j0 < w1; j0 += 64) {
-        const int j = j0 + lane;
-        const uint32_t u = j < w1 ? order_key(w[j]) : 0u;
-        const bool is_tie = j < w1 && tied(j, u);
-        const uint64_t tb = __builtin_amdgcn_ballot_w64(is_tie);
-        const bool keep = j < w1 && (above(j, u) || (is_tie && ties + __popcll(tb & below) < need));
-        const uint64_t kb = __builtin_amdgcn_ballot_w64(keep);
-        if (keep) kept[at + __popcll(kb & below)] = j;
-        at += __popcll(kb);
+    for (int i = 0; i < words; ++i) {
+        uint64_t kb, tb;
+        uint32_t k = 0;
+        if constexpr (CAP > 0) {
+            kb = kept_bits[wave * words + i];
+            tb = tied_bits[wave * words + i];
+            k = keys[t0 + 64 * i];
+        } else {
+            const int j = t0 + 64 * i;
+            k = j < late ? order_key(w[j]) : 0u;
+            kb = __builtin_amdgcn_ballot_w64(k > pick);
+            tb = __builtin_amdgcn_ballot_w64(k == pick && pick != 0);
+        }
+        const bool tied = (tb >> lane & 1) && ties + __popcll(tb & below) < need;
+        kb |= __builtin_amdgcn_ballot_w64(tied);
         ties += __popcll(tb);
+        if (kb >> lane & 1) {
+            const int to = at + __popcll(kb & below);
+            kept[to] = t0 + 64 * i;
+            if constexpr (CAP > 0) wo[to] = key_value(k);  // in place too: every candidate is in LDS
+        }
+        at += __popcll(kb);
     }
+    for (int i = tid; i < len - late; i += NT) kept[take + i] = late + i;
     for (int i = n + tid; i < a.budget; i += NT) kept[i] = -1;
-    __syncthreads();
-    // weights of the kept tokens, in place too: a token never moves up, and
-    // each round's reads end before its writes begin
-    float* wo = a.w_out + b * a.wo_s[0] + h * a.wo_s[1];
-    for (int i0 = 0; i0 < n; i0 += NT) {
-        const int i = i0 + tid;
-        const float x = i < n ? w[kept[i]] : 0.0f;
+    // the recent tokens' weights (or, without keys in LDS, all): a token never
+    // moves up, and each round's reads end before its writes begin, so that
+    // they may move in place
+    if constexpr (CAP == 0) __syncthreads();
+    for (int i0 = CAP > 0 ? take : 0; i0 < n; i0 += 4 * NT) {
+        float x[4] = {};
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            const int i = i0 + e * NT + tid;
+            if (CAP > 0 && i0 == take) x[e] = recent[e];
+            else x[e] = i >= n ? 0.0f : w[CAP > 0 ? late + i - take : kept[i]];
+        }
         __syncthreads();
-        if (i < n) wo[i] = x;
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (i0 + e * NT + tid < n) wo[i0 + e * NT + tid] = x[e];
+        __syncthreads();
     }
     __syncthreads();
     for (int i = n + tid; i < a.w_cols; i += NT) wo[i] = 0.0f;
     if (h == 0 && tid == 0) a.new_lens[b] = n;
 }
 
-// sdpa_cache_move_kernel: one workgroup per page moved to, and k or v. The
-// page's scale is the largest of its tokens' scales; slots past the kept
-// tokens hold zeros.
+// sdpa_cache_move_kernel: one workgroup per (page moved to, key head). The
+// page's scales are the largest of its tokens' scales; slots past the kept
+// tokens hold zeros. k rows move as 16-byte pieces. The bytes of a v token lie
+// `page` apart, so that every cache line of a v page that keeps a token is
+// read whatever the access: these pages are staged in LDS whole (kept tokens
+// are ordered, so few pages hold them), in batches of MOVE_STAGE bytes, and
+// the tokens' columns picked there. The chain kept -> table -> scale -> page
+// of dependent loads is gone through once for k and v together, and the loads
+// of k and of the first batch of v are in flight at once.
+constexpr int MOVE_STAGE = 32 * 1024;
+
+template <int D, int P>
 __global__ __attribute__((amdgpu_flat_work_group_size(256, 256)))
 void sdpa_cache_move_kernel(const CacheArgs a) {
-    __shared__ int src_page[128], src_off[128];
-    __shared__ float ratio[128];
-    __shared__ float red[4];
-    const int tid = threadIdx.x;
+    __shared__ __attribute__((aligned(16))) uint8_t stage[MOVE_STAGE];
+    __shared__ int src_slot[P], src_off[P], page_list[P];
+    __shared__ float rk[P], rv[P];
+    __shared__ float redk[2], redv[2];
+    __shared__ int firsts[2];
+    constexpr int LOG = P == 16 ? 4 : P == 32 ? 5 : P == 64 ? 6 : 7;
+    const int tid = threadIdx.x, lane = tid & 63;
     int id = blockIdx.x;
-    const int is_v = id & 1;
-    id >>= 1;
     const int h = id % a.Hkv;
     id /= a.Hkv;
-    const int b = id % a.B, i0 = (id / a.B) * a.page;
+    const int b = id % a.B, i0 = (id / a.B) * P;
     const int len = (int)min((int64_t)held_tokens(a, b), (int64_t)a.w_cols);
-    const int n = min(min(len, a.budget) - i0, a.page);
+    const int n = min(min(len, a.budget) - i0, P);
     if (n <= 0) return;
-    const int to = a.to[b * a.to_s + i0 / a.page];
+    const int to = a.to[b * a.to_s + i0 / P];
     if (to < 0 || to >= a.n_pages) return;
-    const float* const scales = is_v ? a.vs : a.ks;
-    float top = 0.0f;
-    if (tid < a.page) {
-        int page = -1, off = 0;
-        float sc = 0.0f;
+    if (tid < 128) {  // the first two waves: the page's tokens
+        float sk = 0.0f, sv = 0.0f;
+        int page = -1;
+        bool first = false;  // this token is the first of its source page
         if (tid < n) {
-            const int j = a.kept[((int64_t)b * a.Hkv + h) * a.budget + i0 + tid];
-            page = a.table[b * a.table_s + (j >> a.page_log2)];
-            off = j & (a.page - 1);
-            if (page < 0 || page >= a.n_pages) page = -1;
-            else sc = scales[(int64_t)page * a.Hkv + h];
+            const int* const kp = a.kept + ((int64_t)b * a.Hkv + h) * a.budget + i0;
+            const int j = kp[tid], before = tid > 0 ? kp[tid - 1] : -1;
+            first = tid == 0 || (j >> LOG) != (before >> LOG);
+            page = a.table[b * a.table_s + (j >> LOG)];
+            if (page < 0 || page >= a.n_pages) {
+                page = -1;
+            } else {
+                sk = a.ks[(int64_t)page * a.Hkv + h];
+                sv = a.vs[(int64_t)page * a.Hkv + h];
+            }
+            src_off[tid] = j & (P - 1);
         }
-        src_page[tid] = page;
-        src_off[tid] = off;
-        ratio[tid] = sc;
-        top = sc;
+        if (tid < P) {
+            rk[tid] = sk;
+            rv[tid] = sv;
+        }
+        // number the source pages in order
+        const uint64_t fb = __builtin_amdgcn_ballot_w64(first);
+        const int slot = __popcll(fb & ((uint64_t(2) << lane) - 1)) - 1;
+        if (lane == 0) firsts[tid >> 6] = __popcll(fb);
+#pragma unroll
+        for (int k = 1; k < 64; k *= 2) {
+            sk = fmaxf(sk, __shfl_xor(sk, k));
+            sv = fmaxf(sv, __shfl_xor(sv, k));
+        }
+        if (lane == 0) {
+            redk[tid >> 6] = sk;
+            redv[tid >> 6] = sv;
+        }
+        // the second wave numbers from 64 on for now (its pages follow the first's 64 at most)
+        if (tid < P) src_slot[tid] = tid < n ? slot : -1;
+        if (first) page_list[P > 64 && tid >= 64 ? 64 + slot : slot] = page;
+    }
+    __syncthreads();
+    const int n_lo = firsts[0];
+    const float top_k = fmaxf(fmaxf(redk[0], redk[1]), SCALE_MIN), top_v = fmaxf(fmaxf(redv[0], redv[1]), SCALE_MIN);
+    const float inv_k = inverse(top_k), inv_v = inverse(top_v);
+    // source page number p: page_list[p], or past n_lo the second wave's (a
+    // token whose page began in the first wave has slot -1 there: page n_lo - 1)
+    auto page_of = [&](int p) SDPA_INLINE -> int { return P > 64 && p >= n_lo ? page_list[64 + p - n_lo] : page_list[p]; };
+    auto slot_of = [&](int t) SDPA_INLINE -> int {
+        return t >= n ? -1 : P > 64 && t >= 64 ? n_lo + src_slot[t] : src_slot[t];
+    };
+    const int n_src = n_lo + (P > 64 ? firsts[1] : 0);
+    if (tid == 0) {
+        a.ks[(int64_t)to * a.Hkv + h] = top_k;
+        a.vs[(int64_t)to * a.Hkv + h] = top_v;
+    }
+    constexpr int BYTES = D * P, CHUNKS = BYTES / 16;
+    constexpr int BATCH = MOVE_STAGE / BYTES < P ? MOVE_STAGE / BYTES : P;  // v pages staged at a time
+    constexpr int NL = (BATCH * CHUNKS + 255) / 256;                         // 16-byte loads of a thread
+    constexpr int PER = D / 16, NK = (CHUNKS + 255) / 256;                   // pieces of a k row, pieces of a thread
+    u32x4 kx[NK];
+#pragma unroll
+    for (int k = 0; k < NK; ++k) {
+        const int i = tid + 256 * k, t = i / PER, sl = i < CHUNKS ? slot_of(t) : -1;
+        const int pg = sl < 0 ? -1 : page_of(sl);
+        kx[k] = u32x4{};
+        if (pg >= 0)
+            kx[k] = *reinterpret_cast<const u32x4*>(a.k + (((int64_t)pg * a.Hkv + h) * P + src_off[t]) * D + 16 * (i % PER));
+    }
+    // thread: token t of the page, v columns d0, d0 + STEP, ...
+    constexpr int STEP = 256 / P, NC = D / STEP, G = NC < 4 ? NC : 4;
+    const int t = tid % P, d0 = tid / P;
+    const int mine = slot_of(t);
+    const bool exists = mine >= 0 && page_of(max(mine, 0)) >= 0;
+    const float f = rv[t] * inv_v;
+    uint32_t col[(NC + 3) / 4];
+#pragma unroll
+    for (int k = 0; k < (NC + 3) / 4; ++k) col[k] = 0u;
+    for (int s0 = 0; s0 < n_src; s0 += BATCH) {
+        const int m = min(BATCH, n_src - s0);
+        u32x4 x[NL];
+#pragma unroll
+        for (int k = 0; k < NL; ++k) {
+            const int i = tid + 256 * k;
+            const int64_t pg = max(page_of(s0 + min(i / CHUNKS, m - 1)), 0);
+            if (i < m * CHUNKS) x[k] = reinterpret_cast<const u32x4*>(a.v + (pg * a.Hkv + h) * BYTES)[i % CHUNKS];
+        }
+#pragma unroll
+        for (int k = 0; k < NL; ++k)
+            if (tid + 256 * k < m * CHUNKS) reinterpret_cast<u32x4*>(stage)[tid + 256 * k] = x[k];
+        __syncthreads();
+        if (exists && mine >= s0 && mine < s0 + m) {
+            const uint8_t* const p = stage + (mine - s0) * BYTES + src_off[t];
+#pragma unroll
+            for (int k = 0; k < NC; k += G) {
+                uint32_t c = 0;
+#pragma unroll
+                for (int e = 0; e < G; ++e) c |= (uint32_t)p[(d0 + (k + e) * STEP) * P] << (8 * e);
+                col[k / 4] = f != 1.0f ? rescale4(c, f) : c;
+            }
+        }
+        __syncthreads();
+    }
+    uint8_t* const kd = a.k + ((int64_t)to * a.Hkv + h) * BYTES;
+    uint8_t* const vd = a.v + ((int64_t)to * a.Hkv + h) * BYTES;
+#pragma unroll
+    for (int k = 0; k < NK; ++k) {
+        const int i = tid + 256 * k;
+        if (i >= CHUNKS) break;
+        const float fk = rk[i / PER] * inv_k;
+        if (fk != 1.0f)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) kx[k][e] = rescale4(kx[k][e], fk);
+        reinterpret_cast<u32x4*>(kd)[i] = kx[k];
     }
 #pragma unroll
-    for (int k = 1; k < 64; k *= 2) top = fmaxf(top, __shfl_xor(top, k));
-    if ((tid & 63) == 0) red[tid >> 6] = top;
+    for (int k = 0; k < NC; ++k) stage[(d0 + k * STEP) * P + t] = (uint8_t)(col[k / 4] >> (8 * (k % 4)));
     __syncthreads();
-    top = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-    top = fmaxf(top, SCALE_MIN);
-    const float inv = inverse(top);
-    const uint8_t* const src = is_v ? a.v : a.k;
-    uint8_t* const dst = (is_v ? a.v : a.k) + ((int64_t)to * a.Hkv + h) * a.page * a.D;
-    if (!is_v) {
-        const int per = a.D / 4;
-        for (int i = tid; i < a.page * per; i += 256) {
-            const int t = i / per, c = i - t * per;
-            uint32_t x = 0;
-            if (src_page[t] >= 0) {
-                x = *reinterpret_cast<const uint32_t*>(src + (((int64_t)src_page[t] * a.Hkv + h) * a.page + src_off[t]) * a.D + 4 * c);
-                x = rescale4(x, ratio[t] * inv);
-            }
-            *reinterpret_cast<uint32_t*>(dst + t * a.D + 4 * c) = x;
-        }
-    } else {
-        for (int i = tid; i < a.page * a.D; i += 256) {
-            const int d = i / a.page, t = i - d * a.page;
-            uint32_t x = 0;
-            if (src_page[t] >= 0) {
-                x = src[(((int64_t)src_page[t] * a.Hkv + h) * a.D + d) * a.page + src_off[t]];
-                x = rescale4(x, ratio[t] * inv) & 0xffu;
-            }
-            dst[d * a.page + t] = (uint8_t)x;
-        }
+#pragma unroll
+    for (int k = 0; k < NK; ++k) {
+        const int i = tid + 256 * k;
+        if (i < CHUNKS) reinterpret_cast<u32x4*>(vd)[i] = reinterpret_cast<const u32x4*>(stage)[i];
     }
-    if (tid == 0) (is_v ? a.vs : a.ks)[(int64_t)to * a.Hkv + h] = top;
+}
+
+template <int D>
+static int launch_move(const CacheArgs& a, hipStream_t s) {
+    const dim3 grid((uint32_t)a.B * a.Hkv * a.to_pages), block(256);
+    switch (a.page) {
+        case 16: sdpa_cache_move_kernel<D, 16><<<grid, block, 0, s>>>(a); break;
+        case 32: sdpa_cache_move_kernel<D, 32><<<grid, block, 0, s>>>(a); break;
+        case 64: sdpa_cache_move_kernel<D, 64><<<grid, block, 0, s>>>(a); break;
+        default: sdpa_cache_move_kernel<D, 128><<<grid, block, 0, s>>>(a); break;
+    }
+    return (int)hipGetLastError();
 }
 
 int launch_cache_evict(const CacheArgs& a, void* stream) {
     hipStream_t s = static_cast<hipStream_t>(stream);
-    sdpa_cache_select_kernel<<<dim3(a.B * a.Hkv), dim3(SELECT_THREADS), 0, s>>>(a);
+    // lengths are at most the weights' row and the table's pages
+    const int64_t pages = (int64_t)a.max_pages * a.page, most = a.w_cols < pages ? a.w_cols : pages;
+    const dim3 grid(a.B * a.Hkv), block(SELECT_THREADS);
+    if (most <= 4096) sdpa_cache_select_kernel<4096><<<grid, block, 0, s>>>(a);
+    else if (most <= 16384) sdpa_cache_select_kernel<16384><<<grid, block, 0, s>>>(a);
+    else if (most <= 32768) sdpa_cache_select_kernel<32768><<<grid, block, 0, s>>>(a);
+    else sdpa_cache_select_kernel<0><<<grid, block, 0, s>>>(a);
     int e = (int)hipGetLastError();
     if (e || a.to_pages == 0) return e;
-    sdpa_cache_move_kernel<<<dim3(2u * a.B * a.Hkv * a.to_pages), dim3(256), 0, s>>>(a);
-    return (int)hipGetLastError();
+    return a.D == 32 ? launch_move<32>(a, s) : a.D == 64 ? launch_move<64>(a, s) : launch_move<128>(a, s);
 }
 
 }  // namespace sdpa
