@@ -250,7 +250,10 @@ void sdpa_cache_attention_kernel(const CacheArgs a) {
     id /= a.row_blocks;
     const int h = id % a.Hkv;
     id /= a.Hkv;
-    const int b = id % a.B, range = id / a.B;
+    // the order of the sequences moves on by one with every range: the ids of
+    // an XCD go to its shader engines in turn, and the ranges past a short
+    // sequence's end should not always fall to the same ones
+    const int range = id / a.B, b = (id + range) % a.B;
     const CacheSeq s = cache_sequence(a, b);
     const int rows = s.n * a.group;
     if (rblk * ROWS >= rows) return;
@@ -818,7 +821,7 @@ void sdpa_cache_move_kernel(const CacheArgs a) {
     int id = blockIdx.x;
     const int h = id % a.Hkv;
     id /= a.Hkv;
-    const int b = id % a.B, i0 = (id / a.B) * P;
+    const int b = (id + id / a.B) % a.B, i0 = (id / a.B) * P;  // rotated, as the attention's ranges
     const int len = (int)min((int64_t)held_tokens(a, b), (int64_t)a.w_cols);
     const int n = min(min(len, a.budget) - i0, P);
     if (n <= 0) return;

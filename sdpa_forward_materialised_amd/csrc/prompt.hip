@@ -45,16 +45,26 @@ __device__ __forceinline__ typename Tr<T>::vec load_operand(rsrc_t r, uint32_t o
 
 // Workgroup id -> (block counted from the heaviest, sequence, head): blocks
 // of the same index are neighbours (heaviest first over the whole grid), and
-// the ids that land on one XCD (id % 8) share key heads.
+// the ids that land on one XCD (id % 8) share key heads. Within an XCD ids go
+// to its shader engines in turn, so the order of a row's (sequence, head)
+// pairs moves on by one with every block: without that, the empty workgroups
+// of a short sequence in a ragged batch always fall to the same engines, whose
+// CUs then stay idle (two sequences of 12289 and 5003 tokens, 16 heads of 128:
+// PROMPT_ROT).
 struct PackWork {
     int b, h, blk;
 };
 __device__ __forceinline__ PackWork pack_work(int id, int B, int H, int n_blk) {
     const int n = B * H;
-    int r = id % n;
     PackWork w;
     w.blk = id / n;
-    if (n % 8 == 0) r = (r & 7) * (n >> 3) + (r >> 3);
+    int r = id % n;
+    if (n % 8 == 0) {
+        const int per = n >> 3;
+        r = (r & 7) * per + ((r >> 3) + w.blk) % per;
+    } else {
+        r = (r + w.blk) % n;
+    }
     w.h = r / B;
     w.b = r - w.h * B;
     return w;
@@ -278,11 +288,289 @@ void sdpa_prompt_kernel(const PackArgs a) {
     }
 }
 
-int prompt_block_rows(int dtype, int D) { return dtype == DT_F32 ? PromptCfg<float, 32>::QB : PromptCfg<__bf16, 128>::QB; }
+// The same for 16-bit types and many rows: 64 rows a wave (two 32-row blocks
+// that share every K and V operand read from LDS: with one block a wave the
+// operand reads alone take the LDS as long as the products take the matrix
+// units), 256 rows a workgroup, and the three parts of neighbouring 32-key
+// blocks run interleaved, one wave keeping matrix and vector units busy at
+// once: step j does the exponentials of block j between the products
+// S(j + 1) = K Q^T and A += V P(j - 1)^T. Row references are whole numbers, so
+// that the weights P(j - 1), rounded already, scale exactly when a reference
+// rises in step j.
+#ifndef AHD
+#define AHD 2
+#endif
+#ifndef WIDE_RB
+#define WIDE_RB 1
+#endif
+template <typename T, int D>
+struct WideCfg {
+    static constexpr int NW = 4, RB = WIDE_RB, TN = 64;
+    using C = TwoPassCfg<T, D, NW, MASK_NONE, true, TN, true>;
+    static constexpr int QB = 32 * RB * NW;
+    static constexpr int LDS_BYTES = 4 * C::TILEB;
+};
+
+template <typename T, int D>
+__global__ __attribute__((amdgpu_flat_work_group_size(256, 256), amdgpu_waves_per_eu(WIDE_RB == 2 ? 1 : 2)))
+void sdpa_prompt_wide_kernel(const PackArgs a) {
+    using P = WideCfg<T, D>;
+    using C = typename P::C;
+    using TR = Tr<T>;
+    using vec = typename TR::vec;
+    constexpr int SZ = 2, RB = P::RB, NW = P::NW, TN = P::TN, ND = D / 32, NKS = D / 16;
+    constexpr int SLOTS = RB * NKS, EPS = 16 * RB / SLOTS;  // products of each kind in a step; exponentials per slot
+    __shared__ __attribute__((aligned(16))) uint8_t smem[P::LDS_BYTES];
+
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int n = lane & 31, hf = lane >> 5;
+    const PackWork w = pack_work(blockIdx.x, a.B, a.Hq, a.n_blk);
+    const Seq s = sequence(a, w.b);
+    const int q0 = (a.n_blk - 1 - w.blk) * P::QB;
+    if (q0 >= s.nq) return;
+    const int kend = a.causal ? min(s.nk, max(0, min(q0 + P::QB, s.nq) + s.coff)) : s.nk;
+    const int ntiles = (kend + TN - 1) / TN;
+    const int hk = w.h / a.group;
+
+    const rsrc_t qr = make_rsrc(static_cast<const T*>(a.q) + s.q0 * a.q_s[1] + w.h * a.q_s[0], a.q_ext);
+    const rsrc_t kr = make_rsrc(static_cast<const T*>(a.k) + s.k0 * a.k_s[1] + hk * a.k_s[0], a.k_ext);
+    const rsrc_t vr = make_rsrc(static_cast<const T*>(a.v) + s.k0 * a.v_s[1] + hk * a.v_s[0], a.v_ext);
+    const rsrc_t orr = make_rsrc(static_cast<T*>(a.o) + s.q0 * a.o_s[1] + w.h * a.o_s[0], a.o_ext);
+    const rsrc_t lr = make_rsrc(a.lse + s.q0 * a.l_s[1] + w.h * a.l_s[0], a.l_ext);
+    const uint32_t krow = (uint32_t)(a.k_s[1] * SZ), vrow = (uint32_t)(a.v_s[1] * SZ);
+
+    // K tiles in buffers 0 and 1, V tiles in 2 and 3. A wave's loads of a tile
+    // lie NW * RPI rows apart, where the layouts' chunk order repeats: one
+    // lane offset each for K and V, the rest is uniform.
+    constexpr int LROWS = NW * C::RPI;
+    static_assert(C::fk(LROWS) == 0 && C::fv(LROWS) == 0, "the chunk order repeats from one load to the next");
+    const int lrow = wave * C::RPI + lane / C::CPR;
+    const uint32_t kvo = lrow * krow + ((lane % C::CPR) ^ C::fk(lrow)) * 16;
+    const uint32_t vvo = lrow * vrow + ((lane % C::CPR) ^ C::fv(lrow)) * 16;
+    auto load_tile = [&](rsrc_t r, uint8_t* dst, int t, uint32_t vo, uint32_t row) SDPA_INLINE {
+        const int limit = s.nk - t * TN;
+#pragma unroll
+        for (int jj = 0; jj < C::NI / NW; ++jj)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(dst + (jj * NW + wave) * 1024), 16,
+                                                     pred(lrow + jj * LROWS < limit, vo + (uint32_t)(t * TN + jj * LROWS) * row),
+                                                     0, 0, 0);
+    };
+    auto load_k = [&](int t) SDPA_INLINE { load_tile(kr, smem + (t & 1) * C::TILEB, t, kvo, krow); };
+    auto load_v = [&](int t) SDPA_INLINE { load_tile(vr, smem + (2 + (t & 1)) * C::TILEB, t, vvo, vrow); };
+
+    const int qw = q0 + wave * 32 * RB;  // this wave's first row
+    vec qf[RB][NKS];
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb) {
+        const int qi = qw + 32 * rb + n;
+        const bool ok = qi < s.nq;
+        const uint32_t qoff = (uint32_t)((ok ? qi : 0) * a.q_s[1] * SZ);
+#pragma unroll
+        for (int c = 0; c < NKS; ++c) qf[rb][c] = load_operand<T>(qr, pred(ok, qoff + (c * 16 + hf * 8) * SZ), a.q_mul);
+    }
+    f32x16 oacc[RB][ND], sc[2][RB];  // sc[j & 1]: scores of block j
+    vec pv[2][RB][2];                // pv[j & 1]: weights of block j
+    float m[RB], l[RB];
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb) {
+        m[rb] = -INFINITY;
+        l[rb] = 0.0f;
+#pragma unroll
+        for (int d = 0; d < ND; ++d) oacc[rb][d] = f32x16{};
+    }
+    const int kr0 = swap23(n);
+    const int trg = lane >> 4, trs = lane & 15;
+    const int tr_row = 8 * (trg >> 1) + (trs >> 2);
+    const int tr_col = 16 * (trg & 1) + 4 * (((trs & 1) << 1) | ((trs >> 1) & 1));
+    auto k_op = [&](const uint8_t* kt, int half, int c) SDPA_INLINE -> vec {
+        return *reinterpret_cast<const vec*>(kt + C::pos_k(32 * half + kr0, 2 * c + hf) * 16);
+    };
+    auto v_op = [&](const uint8_t* vt, int half, int kc, int d) SDPA_INLINE -> vec {
+        u32x2 x[2];
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int row = 32 * half + 16 * kc + tr_row + 4 * r, col = 32 * d + tr_col;
+            x[r] = lds_read_tr16(vt + C::pos_v(row, col * SZ / 16) * 16 + ((col * SZ) & 15));
+        }
+        return __builtin_bit_cast(vec, u32x4{x[0][0], x[0][1], x[1][0], x[1][1]});
+    };
+
+    // Step j (its parity PAR): exponentials of block j, with QK the scores of
+    // block j + 1 from K half KH of kt, with PV the sum of block j - 1 from V
+    // half VH of vt. edge: block j holds keys that some row does not keep.
+    auto step = [&](auto par_c, auto exp_c, auto qk_c, auto pv_c, bool edge, int j, const uint8_t* kt, const uint8_t* vt)
+        SDPA_INLINE {
+        constexpr int PAR = decltype(par_c)::value;
+        constexpr bool EXP = decltype(exp_c)::value, QK = decltype(qk_c)::value, PV = decltype(pv_c)::value;
+        // K half of block j + 1 and V half of block j - 1
+        constexpr int KH = (PAR + 1) & 1, VH = (PAR + 1) & 1;
+        constexpr int AHEAD = AHD;  // operands read ahead of their product
+        vec ka[NKS], va[2 * ND];
+        if constexpr (QK)
+#pragma unroll
+            for (int c = 0; c < (AHEAD < NKS ? AHEAD : NKS); ++c) ka[c] = k_op(kt, KH, c);
+        if constexpr (PV)
+#pragma unroll
+            for (int c = 0; c < (AHEAD < 2 * ND ? AHEAD : 2 * ND); ++c) va[c] = v_op(vt, VH, c / ND, c % ND);
+        float mu[RB], sum[RB] = {};
+        if constexpr (EXP) {
+            float top[RB];
+            bool grow = false;
+            if (edge)
+#pragma unroll
+                for (int rb = 0; rb < RB; ++rb) {
+                    const int qi = qw + 32 * rb + n;
+                    const int lim = min(s.nk - 1 - 32 * j, a.causal ? qi + s.coff - 32 * j : 0x7fffffff) - 8 * hf;
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) sc[PAR][rb][r] = kk(0, r) > lim ? -INFINITY : sc[PAR][rb][r];
+                }
+#pragma unroll
+            for (int rb = 0; rb < RB; ++rb) {
+                const f32x16& x = sc[PAR][rb];
+                float y = fmaxf(fmaxf(x[0], x[1]), x[2]);
+#pragma unroll
+                for (int r = 3; r < 15; r += 2) y = fmaxf(fmaxf(y, x[r]), x[r + 1]);
+                top[rb] = fmaxf(y, x[15]) * a.scale_log2;
+                grow = grow || top[rb] > m[rb] + 8.0f;
+            }
+            if (__builtin_amdgcn_ballot_w64(grow) != 0) {
+#pragma unroll
+                for (int rb = 0; rb < RB; ++rb) {
+                    const float up = fmaxf(m[rb], __builtin_ceilf(fmaxf(top[rb], __shfl_xor(top[rb], 32))));
+                    const float f = up == -INFINITY ? 1.0f : fast_exp2(m[rb] - up);
+                    m[rb] = up;
+                    l[rb] *= f;
+#pragma unroll
+                    for (int d = 0; d < ND; ++d)
+#pragma unroll
+                        for (int r = 0; r < 16; ++r) oacc[rb][d][r] *= f;
+                    if constexpr (PV) {
+#pragma unroll
+                        for (int kc = 0; kc < 2; ++kc) {
+                            const u32x4 b = __builtin_bit_cast(u32x4, pv[1 - PAR][rb][kc]);
+                            float x[8];
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) x[e] = TR::to_f((b[e >> 1] >> (16 * (e & 1))) & 0xffffu) * f;
+                            pv[1 - PAR][rb][kc] = TR::cvt8(x);
+                        }
+                    }
+                }
+            }
+#pragma unroll
+            for (int rb = 0; rb < RB; ++rb) mu[rb] = m[rb] == -INFINITY ? 0.0f : -m[rb];
+        }
+        if constexpr (QK)
+#pragma unroll
+            for (int rb = 0; rb < RB; ++rb) sc[1 - PAR][rb] = f32x16{};
+        __builtin_amdgcn_sched_barrier(0);
+        float p[16 * RB];
+#pragma unroll
+        for (int i = 0; i < SLOTS; ++i) {
+            const int rb = i % RB, c = i / RB;
+            if constexpr (QK) {
+                sc[1 - PAR][rb] = TR::mfma(ka[c], qf[rb][c], sc[1 - PAR][rb]);
+                if (rb == 0 && c + AHEAD < NKS) ka[c + AHEAD] = k_op(kt, KH, c + AHEAD);
+            }
+            if constexpr (PV) {
+                oacc[rb][c % ND] = TR::mfma(va[c], pv[1 - PAR][rb][c / ND], oacc[rb][c % ND]);
+                if (rb == RB - 1 && c + AHEAD < 2 * ND) va[c + AHEAD] = v_op(vt, VH, (c + AHEAD) / ND, (c + AHEAD) % ND);
+            }
+            if constexpr (EXP) {
+#pragma unroll
+                for (int e = i * EPS; e < (i + 1) * EPS; ++e) {
+                    p[e] = fast_exp2(__builtin_fmaf(sc[PAR][e >> 4][e & 15], a.scale_log2, mu[e >> 4]));
+                    sum[e >> 4] += p[e];
+                    if (e % 8 == 7) {
+                        // opaque: the compiler would carry the eight floats into the next step and round them there
+                        u32x4 b = __builtin_bit_cast(u32x4, TR::cvt8(p + (e & ~7)));
+                        asm volatile("" : "+v"(b));
+                        pv[PAR][e >> 4][(e >> 3) & 1] = as_vec<T>(b);
+                    }
+                }
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        if constexpr (EXP)
+#pragma unroll
+            for (int rb = 0; rb < RB; ++rb) l[rb] += sum[rb];
+    };
+    static_assert(2 * ND == NKS, "as many V as K operands in a step");
+
+    // tiles before t_full hold kept keys only, for every row of the wave;
+    // tiles from t_end on none
+    const int last_row = min(qw + 32 * RB, s.nq) - 1;
+    const bool live = qw < s.nq;
+    const int t_end = !live ? 0 : a.causal ? max(0, min(ntiles, (last_row + s.coff + TN) / TN)) : ntiles;
+    const int t_full = min(t_end, (a.causal ? max(0, min(s.nk, qw + s.coff + 1)) : s.nk) / TN);
+    constexpr std::integral_constant<int, 0> even{};
+    constexpr std::integral_constant<int, 1> odd{};
+    constexpr std::true_type on{};
+    constexpr std::false_type off{};
+    // iteration t: K tile t and V tile t - 1 are staged; steps 2 t - 1 and 2 t
+    auto stage = [&](int t) SDPA_INLINE {
+        wait_vmem();
+        __syncthreads();
+        if (t + 1 < ntiles) load_k(t + 1);
+        if (t < ntiles) load_v(t);
+    };
+    auto kt = [&](int t) SDPA_INLINE -> const uint8_t* { return smem + (t & 1) * C::TILEB; };
+    auto vt = [&](int t) SDPA_INLINE -> const uint8_t* { return smem + (2 + ((t - 1) & 1)) * C::TILEB; };
+    if (ntiles > 0) load_k(0);
+    int t = 0;
+    if (t_end > 0) {
+        stage(0);
+        step(odd, off, on, off, false, -1, kt(0), vt(0));
+        step(even, on, on, off, t_full == 0, 0, kt(0), vt(0));
+        for (t = 1; t < t_end; ++t) {
+            stage(t);
+            step(odd, on, on, on, t > t_full, 2 * t - 1, kt(t), vt(t));
+            step(even, on, on, on, t >= t_full, 2 * t, kt(t), vt(t));
+        }
+        stage(t);
+        step(odd, on, off, on, t > t_full, 2 * t - 1, kt(t), vt(t));
+        step(even, off, off, on, false, 2 * t, kt(t), vt(t));
+        ++t;
+    }
+    for (; t <= ntiles; ++t) stage(t);
+
+#pragma unroll
+    for (int rb = 0; rb < RB; ++rb) {
+        const int qi = qw + 32 * rb + n;
+        const bool ok = qi < s.nq;
+        const float sum = l[rb] + __shfl_xor(l[rb], 32);
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        const uint32_t ooff = (uint32_t)((ok ? qi : 0) * a.o_s[1] * SZ);
+#pragma unroll
+        for (int d = 0; d < ND; ++d) {
+            float x[16];
+#pragma unroll
+            for (int r = 0; r < 16; ++r) x[r] = oacc[rb][d][r] * inv;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                if (a.o_vec) store8<T, true>(orr, ooff, ok, 32 * d + 16 * c + 8 * hf, D, x + 8 * c);
+                else store8<T, false>(orr, ooff, ok, 32 * d + 16 * c + 8 * hf, D, x + 8 * c);
+            }
+        }
+        const float lse = sum == 0.0f ? -INFINITY : (m[rb] + __builtin_amdgcn_logf(sum)) * LN2;
+        __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, lse), lr,
+                                              pred(ok && hf == 0, (uint32_t)((ok ? qi : 0) * a.l_s[1] * 4)), 0, 0);
+    }
+}
 
 template <typename T>
 static int launch_prompt_t(int D, const PackArgs& a, hipStream_t s) {
     const dim3 grid((uint32_t)a.B * a.Hq * a.n_blk), block(256);
+    if constexpr (sizeof(T) == 2) {
+        if (a.wide) {
+            switch (D) {
+                case 32: sdpa_prompt_wide_kernel<T, 32><<<grid, block, 0, s>>>(a); break;
+                case 64: sdpa_prompt_wide_kernel<T, 64><<<grid, block, 0, s>>>(a); break;
+                case 128: sdpa_prompt_wide_kernel<T, 128><<<grid, block, 0, s>>>(a); break;
+                default: return (int)hipErrorInvalidValue;
+            }
+            return (int)hipGetLastError();
+        }
+    }
     switch (D) {
         case 32: sdpa_prompt_kernel<T, 32><<<grid, block, 0, s>>>(a); break;
         case 64: sdpa_prompt_kernel<T, 64><<<grid, block, 0, s>>>(a); break;

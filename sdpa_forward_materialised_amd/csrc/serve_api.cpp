@@ -6,6 +6,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <cstdlib>
 #include <cstring>
 
 #include "api_checks.h"
@@ -117,6 +118,14 @@ sdpa_status_t check_cu(int64_t n_seqs, const void* cu_q, const void* cu_k, int i
 sdpa_status_t grid_ok(int64_t n) {
     if (n > INT32_MAX) return fail(SDPA_ERR_UNSUPPORTED, "grid too large");
     return SDPA_OK;
+}
+
+// Prompt attention: the kernel of 256 rows a workgroup for 16-bit types,
+// where its blocks still give every CU one.
+bool prompt_wide(const sdpa::PackArgs& a, int dtype) {
+    if (dtype == SDPA_F32) return false;
+    if (const char* e = std::getenv("SDPA_WIDE")) return e[0] == '1';
+    return (int64_t)a.B * a.Hq * cdiv(a.max_q, sdpa::PROMPT_WIDE_ROWS) >= 256;
 }
 
 // Key weights: ranges of one query head's rows. A key block's work is a range
@@ -309,7 +318,8 @@ sdpa_status_t sdpa_prompt_fwd(const sdpa_tensor_t* q, const sdpa_tensor_t* k, co
     TRY(pack_extent(out, "out", a.max_q, out->sizes[2], &a.o_ext));
     TRY(pack_extent(lse, "lse", a.max_q, 1, &a.l_ext));
     const int D = (int)q->sizes[2];
-    a.n_blk = (int)cdiv(a.max_q, sdpa::prompt_block_rows(q->dtype, D));
+    a.wide = prompt_wide(a, q->dtype);
+    a.n_blk = (int)cdiv(a.max_q, a.wide ? sdpa::PROMPT_WIDE_ROWS : sdpa::PROMPT_ROWS);
     TRY(grid_ok(n_seqs * a.Hq * a.n_blk));
     return launched(sdpa::launch_prompt(q->dtype, D, a, hip_stream));
 }

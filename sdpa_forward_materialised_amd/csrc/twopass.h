@@ -101,8 +101,8 @@ struct TwoPassCfg {
     //  V: 4 rows x 2 chunks per 16-lane group of the transposing read, the
     //     two groups of a cycle on the other 2 chunks: f moves whole groups
     //     of 4 chunks.
-    static __device__ __forceinline__ int fk(int row) { return (row / RPB) & (CPR - 1); }
-    static __device__ __forceinline__ int fv(int row) { return 4 * ((row / RPB) & (CPR / 4 - 1)); }
+    static __host__ __device__ __forceinline__ constexpr int fk(int row) { return (row / RPB) & (CPR - 1); }
+    static __host__ __device__ __forceinline__ constexpr int fv(int row) { return 4 * ((row / RPB) & (CPR / 4 - 1)); }
     static __device__ __forceinline__ int pos_k(int row, int chunk) { return row * CPR + (chunk ^ fk(row)); }
     static __device__ __forceinline__ int pos_v(int row, int chunk) { return row * CPR + (chunk ^ fv(row)); }
     // staged P tile: row-major, chunks XOR-permuted like K (writes: 16 rows,
