@@ -382,6 +382,46 @@ void sdpa_cache_attention_kernel(const CacheArgs a) {
                     for (int r = 0; r < 4; ++r) oacc[rt][d][r] *= f;
             }
         }
+        if (cut) {
+            // NaN among the values, where a row may not keep it (0 times NaN
+            // would take it in): read as 0, and given to the rows that do
+            uint32_t odd = 0;
+#pragma unroll
+            for (int d = 0; d < ND; ++d)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) odd |= (vc[d][i] & 0x7f7f7f7fu) + 0x01010101u;
+            if (__builtin_amdgcn_ballot_w64((odd & 0x80808080u) != 0) != 0) {
+#pragma unroll
+                for (int rt = 0; rt < RT; ++rt) {
+                    bf16x8 kept[2];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i)
+                        kept[i >> 3][i & 7] = (__bf16)(acc[rt][i >> 2][i & 3] == -INFINITY ? 0.0f : 1.0f);
+#pragma unroll
+                    for (int d = 0; d < ND; ++d) {
+                        f32x4 count = {};
+#pragma unroll
+                        for (int c = 0; c < 2; ++c) {
+                            uint32_t w[2];
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                const uint32_t x = vc[d][2 * c + i];
+                                w[i] = ((((x & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7) * 0x38u;  // 1.0 for NaN
+                            }
+                            count = OB::mfma(OB::widen(w[0], w[1]), kept[c], count);
+                        }
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            if (count[r] != 0.0f) oacc[rt][d][r] = NAN;
+                    }
+                }
+#pragma unroll
+                for (int d = 0; d < ND; ++d)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        vc[d][i] &= ~(((((vc[d][i] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7) * 0xffu);
+            }
+        }
         bf16x8 ph[RT][2], pl[RT][2];
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {

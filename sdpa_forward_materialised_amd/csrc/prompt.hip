@@ -28,18 +28,57 @@ __device__ __forceinline__ Seq sequence(const PackArgs& a, int b) {
     return s;
 }
 
-template <typename T>
-__device__ __forceinline__ typename Tr<T>::vec load_operand(rsrc_t r, uint32_t off, int mul) {
+// Buffer-to-LDS copy of 16 bytes a lane, to lds + 16 lane. Written as assembly
+// (it has no register output), because the compiler, which cannot tell the
+// tile being filled from the tile being read, waits for the builtin's copies
+// before the next LDS read: every tile's loads were waited for as soon as they
+// were issued. Copies are counted in order with the other vector memory
+// operations; wait_copies(n) waits until at most n of them are under way, and
+// stands, with the barrier, between a copy and the first read of its bytes.
+typedef uint32_t desc_t __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ desc_t make_desc(const void* base, uint32_t bytes) {
+    const uint64_t p = reinterpret_cast<uint64_t>(base);
+    return desc_t{(uint32_t)p, (uint32_t)(p >> 32) & 0xffffu, bytes, (uint32_t)RSRC_WORD3};
+}
+__device__ __forceinline__ uint32_t lds_address(const void* p) { return (uint32_t)(uintptr_t)(lds_void*)p; }
+__device__ __forceinline__ void copy_to_lds(desc_t d, uint32_t lds, uint32_t off) {
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"  // m0 is named, though the compiler reserves it
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                 :
+                 : "s"(lds), "v"(off), "s"(d)
+                 : "m0", "memory");
+#pragma clang diagnostic pop
+}
+template <int N>
+__device__ __forceinline__ void wait_copies() {
+    static_assert(N < 16, "the low bits of the counter");
+    __builtin_amdgcn_s_waitcnt(0x0F70 | N);
+}
+
+// An operand of the products from memory: all loads are in flight before the
+// first is touched.
+template <typename T, int N>
+__device__ __forceinline__ void load_operands(rsrc_t r, const uint32_t* off, int mul, typename Tr<T>::vec* out) {
     if constexpr (sizeof(T) == 2) {
-        u32x4 x = ld128(r, off);
+        u32x4 x[N];
+#pragma unroll
+        for (int i = 0; i < N; ++i) x[i] = ld128(r, off[i]);
         if (mul != 1) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[e] = mul == 0 ? 0u : x[e] ^ 0x80008000u;
+            for (int i = 0; i < N; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[i][e] = mul == 0 ? 0u : x[i][e] ^ 0x80008000u;
         }
-        return as_vec<T>(x);
+#pragma unroll
+        for (int i = 0; i < N; ++i) out[i] = as_vec<T>(x[i]);
     } else {
-        const float x = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(r, off, 0, 0));
-        return mul == 1 ? x : mul == 0 ? 0.0f : -x;
+        const float f = (float)mul;
+#pragma unroll
+        for (int i = 0; i < N; ++i) out[i] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(r, off[i], 0, 0));
+        if (mul != 1)
+#pragma unroll
+            for (int i = 0; i < N; ++i) out[i] = mul == 0 ? 0.0f : f * out[i];
     }
 }
 
@@ -50,7 +89,7 @@ __device__ __forceinline__ typename Tr<T>::vec load_operand(rsrc_t r, uint32_t o
 // pairs moves on by one with every block: without that, the empty workgroups
 // of a short sequence in a ragged batch always fall to the same engines, whose
 // CUs then stay idle (two sequences of 12289 and 5003 tokens, 16 heads of 128:
-// PROMPT_ROT).
+// 1011 us without the step, 727 with it).
 struct PackWork {
     int b, h, blk;
 };
@@ -68,6 +107,70 @@ __device__ __forceinline__ PackWork pack_work(int id, int B, int H, int n_blk) {
     w.h = r / B;
     w.b = r - w.h * B;
     return w;
+}
+
+// Values that are not finite, in tiles that hold keys which some row does not
+// keep: a product takes them into every row of its block, kept or not (0 times
+// NaN). Where a block's sums come out not finite, the workgroup takes the block
+// again with such values read as 0 in these tiles (clean_tile), and adds them
+// to the rows that keep their keys at the end (add_kept).
+template <typename T>
+__device__ __forceinline__ uint32_t clean_word(uint32_t w) {
+    if constexpr (sizeof(T) == 4) {
+        return (w & 0x7f800000u) == 0x7f800000u ? 0u : w;
+    } else {
+        constexpr uint32_t E = std::is_same<T, __bf16>::value ? 0x7f80u : 0x7c00u;
+        const uint32_t lo = (w & E) == E ? 0u : w & 0xffffu, hi = ((w >> 16) & E) == E ? 0u : w & 0xffff0000u;
+        return lo | hi;
+    }
+}
+template <typename T, int BYTES>
+__device__ __forceinline__ void clean_tile(uint8_t* tile, int thread) {
+    for (int i = thread; i < BYTES / 16; i += 256) {
+        u32x4 x = reinterpret_cast<u32x4*>(tile)[i];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = clean_word<T>(x[e]);
+        reinterpret_cast<u32x4*>(tile)[i] = x;
+    }
+}
+template <int ND>
+__device__ __forceinline__ bool all_finite(const f32x16* x) {
+    float z = 0.0f;
+#pragma unroll
+    for (int d = 0; d < ND; ++d)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) z = __builtin_fmaf(x[d][r], 0.0f, z);
+    return z == 0.0f;
+}
+// keys [j0, j1) of v; the row keeps j <= last
+template <typename T, int ND>
+__device__ __forceinline__ void add_kept(rsrc_t v, uint32_t row_bytes, int j0, int j1, int last, int hf, f32x16* x) {
+    constexpr int SZ = (int)sizeof(T), W = SZ == 2 ? 4 : 8;
+    for (int j = j0; j < j1; ++j)
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                uint32_t w[W];
+#pragma unroll
+                for (int i = 0; i < W / 4; ++i) {
+                    const u32x4 y = ld128(v, (uint32_t)j * row_bytes + (32 * d + 16 * c + 8 * hf) * SZ + 16 * i);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) w[4 * i + e] = y[e];
+                }
+                bool any = false;
+#pragma unroll
+                for (int i = 0; i < W; ++i) any = any || clean_word<T>(w[i]) != w[i];
+                if (__builtin_amdgcn_ballot_w64(any) == 0) continue;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    float f;
+                    if constexpr (SZ == 2) f = Tr<T>::to_f((w[e >> 1] >> (16 * (e & 1))) & 0xffffu);
+                    else f = __builtin_bit_cast(float, w[e]);
+                    const bool odd = (__builtin_bit_cast(uint32_t, f) & 0x7f800000u) == 0x7f800000u;
+                    if (odd && j <= last) x[d][8 * c + e] += f;
+                }
+            }
 }
 
 template <typename T, int D>
@@ -102,25 +205,23 @@ void sdpa_prompt_kernel(const PackArgs a) {
     const int hk = w.h / a.group;
 
     const rsrc_t qr = make_rsrc(static_cast<const T*>(a.q) + s.q0 * a.q_s[1] + w.h * a.q_s[0], a.q_ext);
-    const rsrc_t kr = make_rsrc(static_cast<const T*>(a.k) + s.k0 * a.k_s[1] + hk * a.k_s[0], a.k_ext);
-    const rsrc_t vr = make_rsrc(static_cast<const T*>(a.v) + s.k0 * a.v_s[1] + hk * a.v_s[0], a.v_ext);
+    const desc_t kd = make_desc(static_cast<const T*>(a.k) + s.k0 * a.k_s[1] + hk * a.k_s[0], a.k_ext);
+    const desc_t vd = make_desc(static_cast<const T*>(a.v) + s.k0 * a.v_s[1] + hk * a.v_s[0], a.v_ext);
     const rsrc_t orr = make_rsrc(static_cast<T*>(a.o) + s.q0 * a.o_s[1] + w.h * a.o_s[0], a.o_ext);
     const rsrc_t lr = make_rsrc(a.lse + s.q0 * a.l_s[1] + w.h * a.l_s[0], a.l_ext);
     const uint32_t krow = (uint32_t)(a.k_s[1] * SZ), vrow = (uint32_t)(a.v_s[1] * SZ);
 
+    const uint32_t lds = lds_address(smem);
     auto load_tile = [&](int t) SDPA_INLINE {
-        uint8_t* const kd = smem + (t & 1) * 2 * C::TILEB;
-        uint8_t* const vd = kd + C::TILEB;
+        const uint32_t kl = lds + (t & 1) * 2 * C::TILEB, vl = kl + C::TILEB;
 #pragma unroll
         for (int jj = 0; jj < C::NI / NW; ++jj) {
             const int j = jj * NW + wave;
             const int row = j * C::RPI + lane / C::CPR;
             const bool ok = t * TN + row < s.nk;
             const int ck = (lane % C::CPR) ^ C::fk(row), cv = (lane % C::CPR) ^ C::fv(row);
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(kr, (lds_void*)(kd + j * 1024), 16, pred(ok, row * krow + ck * 16),
-                                                     (uint32_t)(t * TN) * krow, 0, 0);
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(vr, (lds_void*)(vd + j * 1024), 16, pred(ok, row * vrow + cv * 16),
-                                                     (uint32_t)(t * TN) * vrow, 0, 0);
+            copy_to_lds(kd, kl + j * 1024, pred(ok, (uint32_t)(t * TN + row) * krow + ck * 16));
+            copy_to_lds(vd, vl + j * 1024, pred(ok, (uint32_t)(t * TN + row) * vrow + cv * 16));
         }
     };
     static_assert(C::NI % NW == 0, "tile loads split evenly over the waves");
@@ -133,19 +234,13 @@ void sdpa_prompt_kernel(const PackArgs a) {
         qi[rb] = qw + 32 * rb + n;
         const bool ok = qi[rb] < s.nq;
         const uint32_t qoff = (uint32_t)((ok ? qi[rb] : 0) * a.q_s[1] * SZ);
+        uint32_t off[NKS];
 #pragma unroll
-        for (int c = 0; c < NKS; ++c)
-            qf[rb][c] = load_operand<T>(qr, pred(ok, qoff + (c * KSTEP + hf * TR::KH) * SZ), a.q_mul);
+        for (int c = 0; c < NKS; ++c) off[c] = pred(ok, qoff + (c * KSTEP + hf * TR::KH) * SZ);
+        load_operands<T, NKS>(qr, off, a.q_mul, qf[rb]);
     }
     f32x16 oacc[RB][ND];
     float m[RB], l[RB];
-#pragma unroll
-    for (int rb = 0; rb < RB; ++rb) {
-        m[rb] = -INFINITY;
-        l[rb] = 0.0f;
-#pragma unroll
-        for (int d = 0; d < ND; ++d) oacc[rb][d] = f32x16{};
-    }
     const int kr0 = swap23(n);
     const int trg = lane >> 4, trs = lane & 15;
     const int tr_row = 8 * (trg >> 1) + (trs >> 2);
@@ -254,15 +349,43 @@ void sdpa_prompt_kernel(const PackArgs a) {
     const bool live = qw < s.nq;
     const int t_end = !live ? 0 : a.causal ? max(0, min(ntiles, (last_row + s.coff + TN) / TN)) : ntiles;
     const int t_full = min(t_end, (a.causal ? max(0, min(s.nk, qw + s.coff + 1)) : s.nk) / TN);
-    if (ntiles > 0) load_tile(0);
-    wait_vmem();
-    __syncthreads();
-    for (int t = 0; t < ntiles; ++t) {
-        if (t + 1 < ntiles) load_tile(t + 1);
-        if (t < t_full) tile(t, std::false_type{});
-        else if (t < t_end) tile(t, std::true_type{});
-        wait_vmem();
+    // the first tile with a key that some row of the workgroup does not keep
+    const int t_cut = (a.causal ? max(0, min(s.nk, q0 + s.coff + 1)) : s.nk) / TN;
+    bool again = false;
+    for (;;) {
+#pragma unroll
+        for (int rb = 0; rb < RB; ++rb) {
+            m[rb] = -INFINITY;
+            l[rb] = 0.0f;
+#pragma unroll
+            for (int d = 0; d < ND; ++d) oacc[rb][d] = f32x16{};
+        }
+        if (ntiles > 0) load_tile(0);
+        wait_copies<0>();
         __syncthreads();
+        for (int t = 0; t < ntiles; ++t) {
+            if (again && t >= t_cut) {
+                clean_tile<T, C::TILEB>(smem + ((t & 1) * 2 + 1) * C::TILEB, threadIdx.x);
+                __syncthreads();
+            }
+            if (t + 1 < ntiles) load_tile(t + 1);
+            if (t < t_full) tile(t, std::false_type{});
+            else if (t < t_end) tile(t, std::true_type{});
+            wait_copies<0>();
+            __syncthreads();
+        }
+        if (again || t_cut >= ntiles) break;
+        bool ok = true;
+#pragma unroll
+        for (int rb = 0; rb < RB; ++rb) ok = ok && all_finite<ND>(oacc[rb]);
+        again = __syncthreads_or(!ok) != 0;
+        if (!again) break;
+    }
+    if (again) {
+        const rsrc_t vr = make_rsrc(static_cast<const T*>(a.v) + s.k0 * a.v_s[1] + hk * a.v_s[0], a.v_ext);
+#pragma unroll
+        for (int rb = 0; rb < RB; ++rb)
+            add_kept<T, ND>(vr, vrow, t_cut * TN, kend, a.causal ? qi[rb] + s.coff : s.nk - 1, hf, oacc[rb]);
     }
 
 #pragma unroll
@@ -288,33 +411,32 @@ void sdpa_prompt_kernel(const PackArgs a) {
     }
 }
 
-// The same for 16-bit types and many rows: 64 rows a wave (two 32-row blocks
-// that share every K and V operand read from LDS: with one block a wave the
-// operand reads alone take the LDS as long as the products take the matrix
-// units), 256 rows a workgroup, and the three parts of neighbouring 32-key
-// blocks run interleaved, one wave keeping matrix and vector units busy at
+// The same for 16-bit types, with the three parts of neighbouring 32-key
+// blocks interleaved, so that one wave keeps matrix and vector units busy at
 // once: step j does the exponentials of block j between the products
-// S(j + 1) = K Q^T and A += V P(j - 1)^T. Row references are whole numbers, so
-// that the weights P(j - 1), rounded already, scale exactly when a reference
-// rises in step j.
-#ifndef AHD
-#define AHD 2
-#endif
-#ifndef WIDE_RB
-#define WIDE_RB 1
-#endif
-template <typename T, int D>
+// S(j + 1) = K Q^T and A += V P(j - 1)^T. Nothing waits for a maximum: the
+// exponentials take the reference they find, and only where a lane's sum over
+// a block passes 2^12 (or a row has no reference yet, in its first block) the
+// reference rises to the row's maximum, A and l are scaled and the block's
+// weights taken again, while its scores are still there.
+//
+// NG: groups of four waves. With two, they take the same rows and every other
+// tile each, and join their sums at the end: for calls whose blocks leave the
+// chip's wave slots empty, the chain of tiles is half as long.
+template <typename T, int D, int NG>
 struct WideCfg {
-    static constexpr int NW = 4, RB = WIDE_RB, TN = 64;
+    static constexpr int NW = 4, RB = 1, TN = 64;
     using C = TwoPassCfg<T, D, NW, MASK_NONE, true, TN, true>;
     static constexpr int QB = 32 * RB * NW;
-    static constexpr int LDS_BYTES = 4 * C::TILEB;
+    static constexpr int JOIN_BYTES = NG > 1 ? NW * RB * (D / 32) * 16 * 64 * 4 : 0;  // one group's sums
+    static constexpr int TILE_BYTES = NG * 4 * C::TILEB;
+    static constexpr int LDS_BYTES = TILE_BYTES > JOIN_BYTES ? TILE_BYTES : JOIN_BYTES;
 };
 
-template <typename T, int D>
-__global__ __attribute__((amdgpu_flat_work_group_size(256, 256), amdgpu_waves_per_eu(WIDE_RB == 2 ? 1 : 2)))
+template <typename T, int D, int NG>
+__global__ __attribute__((amdgpu_flat_work_group_size(256 * NG, 256 * NG), amdgpu_waves_per_eu(2)))
 void sdpa_prompt_wide_kernel(const PackArgs a) {
-    using P = WideCfg<T, D>;
+    using P = WideCfg<T, D, NG>;
     using C = typename P::C;
     using TR = Tr<T>;
     using vec = typename TR::vec;
@@ -322,7 +444,10 @@ void sdpa_prompt_wide_kernel(const PackArgs a) {
     constexpr int SLOTS = RB * NKS, EPS = 16 * RB / SLOTS;  // products of each kind in a step; exponentials per slot
     __shared__ __attribute__((aligned(16))) uint8_t smem[P::LDS_BYTES];
 
-    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    __shared__ float2 ml_s[NG > 1 ? NW * 64 * RB : 1];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) % NW;
+    const int grp = NG > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 8) : 0;
+    uint8_t* const buf = smem + grp * 4 * C::TILEB;  // this group's tiles
     const int n = lane & 31, hf = lane >> 5;
     const PackWork w = pack_work(blockIdx.x, a.B, a.Hq, a.n_blk);
     const Seq s = sequence(a, w.b);
@@ -333,8 +458,8 @@ void sdpa_prompt_wide_kernel(const PackArgs a) {
     const int hk = w.h / a.group;
 
     const rsrc_t qr = make_rsrc(static_cast<const T*>(a.q) + s.q0 * a.q_s[1] + w.h * a.q_s[0], a.q_ext);
-    const rsrc_t kr = make_rsrc(static_cast<const T*>(a.k) + s.k0 * a.k_s[1] + hk * a.k_s[0], a.k_ext);
-    const rsrc_t vr = make_rsrc(static_cast<const T*>(a.v) + s.k0 * a.v_s[1] + hk * a.v_s[0], a.v_ext);
+    const desc_t kd = make_desc(static_cast<const T*>(a.k) + s.k0 * a.k_s[1] + hk * a.k_s[0], a.k_ext);
+    const desc_t vd = make_desc(static_cast<const T*>(a.v) + s.k0 * a.v_s[1] + hk * a.v_s[0], a.v_ext);
     const rsrc_t orr = make_rsrc(static_cast<T*>(a.o) + s.q0 * a.o_s[1] + w.h * a.o_s[0], a.o_ext);
     const rsrc_t lr = make_rsrc(a.lse + s.q0 * a.l_s[1] + w.h * a.l_s[0], a.l_ext);
     const uint32_t krow = (uint32_t)(a.k_s[1] * SZ), vrow = (uint32_t)(a.v_s[1] * SZ);
@@ -347,16 +472,17 @@ void sdpa_prompt_wide_kernel(const PackArgs a) {
     const int lrow = wave * C::RPI + lane / C::CPR;
     const uint32_t kvo = lrow * krow + ((lane % C::CPR) ^ C::fk(lrow)) * 16;
     const uint32_t vvo = lrow * vrow + ((lane % C::CPR) ^ C::fv(lrow)) * 16;
-    auto load_tile = [&](rsrc_t r, uint8_t* dst, int t, uint32_t vo, uint32_t row) SDPA_INLINE {
+    auto load_tile = [&](desc_t r, uint32_t dst, int t, uint32_t vo, uint32_t row) SDPA_INLINE {
         const int limit = s.nk - t * TN;
 #pragma unroll
         for (int jj = 0; jj < C::NI / NW; ++jj)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)(dst + (jj * NW + wave) * 1024), 16,
-                                                     pred(lrow + jj * LROWS < limit, vo + (uint32_t)(t * TN + jj * LROWS) * row),
-                                                     0, 0, 0);
+            copy_to_lds(r, dst + (jj * NW + wave) * 1024,
+                        pred(lrow + jj * LROWS < limit, vo + (uint32_t)(t * TN + jj * LROWS) * row));
     };
-    auto load_k = [&](int t) SDPA_INLINE { load_tile(kr, smem + (t & 1) * C::TILEB, t, kvo, krow); };
-    auto load_v = [&](int t) SDPA_INLINE { load_tile(vr, smem + (2 + (t & 1)) * C::TILEB, t, vvo, vrow); };
+    const uint32_t lds = lds_address(buf);
+    auto tile = [&](int u) SDPA_INLINE { return u * NG + grp; };  // this group's tile u
+    auto load_k = [&](int u) SDPA_INLINE { load_tile(kd, lds + (u & 1) * C::TILEB, tile(u), kvo, krow); };
+    auto load_v = [&](int u) SDPA_INLINE { load_tile(vd, lds + (2 + (u & 1)) * C::TILEB, tile(u), vvo, vrow); };
 
     const int qw = q0 + wave * 32 * RB;  // this wave's first row
     vec qf[RB][NKS];
@@ -365,19 +491,14 @@ void sdpa_prompt_wide_kernel(const PackArgs a) {
         const int qi = qw + 32 * rb + n;
         const bool ok = qi < s.nq;
         const uint32_t qoff = (uint32_t)((ok ? qi : 0) * a.q_s[1] * SZ);
+        uint32_t off[NKS];
 #pragma unroll
-        for (int c = 0; c < NKS; ++c) qf[rb][c] = load_operand<T>(qr, pred(ok, qoff + (c * 16 + hf * 8) * SZ), a.q_mul);
+        for (int c = 0; c < NKS; ++c) off[c] = pred(ok, qoff + (c * 16 + hf * 8) * SZ);
+        load_operands<T, NKS>(qr, off, a.q_mul, qf[rb]);
     }
     f32x16 oacc[RB][ND], sc[2][RB];  // sc[j & 1]: scores of block j
     vec pv[2][RB][2];                // pv[j & 1]: weights of block j
     float m[RB], l[RB];
-#pragma unroll
-    for (int rb = 0; rb < RB; ++rb) {
-        m[rb] = -INFINITY;
-        l[rb] = 0.0f;
-#pragma unroll
-        for (int d = 0; d < ND; ++d) oacc[rb][d] = f32x16{};
-    }
     const int kr0 = swap23(n);
     const int trg = lane >> 4, trs = lane & 15;
     const int tr_row = 8 * (trg >> 1) + (trs >> 2);
@@ -404,7 +525,7 @@ void sdpa_prompt_wide_kernel(const PackArgs a) {
         constexpr bool EXP = decltype(exp_c)::value, QK = decltype(qk_c)::value, PV = decltype(pv_c)::value;
         // K half of block j + 1 and V half of block j - 1
         constexpr int KH = (PAR + 1) & 1, VH = (PAR + 1) & 1;
-        constexpr int AHEAD = AHD;  // operands read ahead of their product
+        constexpr int AHEAD = 2;  // operands read ahead of their product
         vec ka[NKS], va[2 * ND];
         if constexpr (QK)
 #pragma unroll
@@ -414,8 +535,6 @@ void sdpa_prompt_wide_kernel(const PackArgs a) {
             for (int c = 0; c < (AHEAD < 2 * ND ? AHEAD : 2 * ND); ++c) va[c] = v_op(vt, VH, c / ND, c % ND);
         float mu[RB], sum[RB] = {};
         if constexpr (EXP) {
-            float top[RB];
-            bool grow = false;
             if (edge)
 #pragma unroll
                 for (int rb = 0; rb < RB; ++rb) {
@@ -425,44 +544,19 @@ void sdpa_prompt_wide_kernel(const PackArgs a) {
                     for (int r = 0; r < 16; ++r) sc[PAR][rb][r] = kk(0, r) > lim ? -INFINITY : sc[PAR][rb][r];
                 }
 #pragma unroll
-            for (int rb = 0; rb < RB; ++rb) {
-                const f32x16& x = sc[PAR][rb];
-                float y = fmaxf(fmaxf(x[0], x[1]), x[2]);
-#pragma unroll
-                for (int r = 3; r < 15; r += 2) y = fmaxf(fmaxf(y, x[r]), x[r + 1]);
-                top[rb] = fmaxf(y, x[15]) * a.scale_log2;
-                grow = grow || top[rb] > m[rb] + 8.0f;
-            }
-            if (__builtin_amdgcn_ballot_w64(grow) != 0) {
-#pragma unroll
-                for (int rb = 0; rb < RB; ++rb) {
-                    const float up = fmaxf(m[rb], __builtin_ceilf(fmaxf(top[rb], __shfl_xor(top[rb], 32))));
-                    const float f = up == -INFINITY ? 1.0f : fast_exp2(m[rb] - up);
-                    m[rb] = up;
-                    l[rb] *= f;
-#pragma unroll
-                    for (int d = 0; d < ND; ++d)
-#pragma unroll
-                        for (int r = 0; r < 16; ++r) oacc[rb][d][r] *= f;
-                    if constexpr (PV) {
-#pragma unroll
-                        for (int kc = 0; kc < 2; ++kc) {
-                            const u32x4 b = __builtin_bit_cast(u32x4, pv[1 - PAR][rb][kc]);
-                            float x[8];
-#pragma unroll
-                            for (int e = 0; e < 8; ++e) x[e] = TR::to_f((b[e >> 1] >> (16 * (e & 1))) & 0xffffu) * f;
-                            pv[1 - PAR][rb][kc] = TR::cvt8(x);
-                        }
-                    }
-                }
-            }
-#pragma unroll
             for (int rb = 0; rb < RB; ++rb) mu[rb] = m[rb] == -INFINITY ? 0.0f : -m[rb];
         }
         if constexpr (QK)
 #pragma unroll
             for (int rb = 0; rb < RB; ++rb) sc[1 - PAR][rb] = f32x16{};
         __builtin_amdgcn_sched_barrier(0);
+        // weights r8 .. r8 + 7 of row block rb
+        auto weights8 = [&](int rb, int r8, const float* p) SDPA_INLINE {
+            // opaque: the compiler would carry the eight floats into the next step and round them there
+            u32x4 b = __builtin_bit_cast(u32x4, TR::cvt8(p));
+            asm volatile("" : "+v"(b));
+            pv[PAR][rb][r8 >> 3] = as_vec<T>(b);
+        };
         float p[16 * RB];
 #pragma unroll
         for (int i = 0; i < SLOTS; ++i) {
@@ -480,19 +574,45 @@ void sdpa_prompt_wide_kernel(const PackArgs a) {
                 for (int e = i * EPS; e < (i + 1) * EPS; ++e) {
                     p[e] = fast_exp2(__builtin_fmaf(sc[PAR][e >> 4][e & 15], a.scale_log2, mu[e >> 4]));
                     sum[e >> 4] += p[e];
-                    if (e % 8 == 7) {
-                        // opaque: the compiler would carry the eight floats into the next step and round them there
-                        u32x4 b = __builtin_bit_cast(u32x4, TR::cvt8(p + (e & ~7)));
-                        asm volatile("" : "+v"(b));
-                        pv[PAR][e >> 4][(e >> 3) & 1] = as_vec<T>(b);
-                    }
+                    if (e % 8 == 7) weights8(e >> 4, e & 8, p + (e & ~7));
                 }
             }
             __builtin_amdgcn_sched_barrier(0);
         }
-        if constexpr (EXP)
+        if constexpr (EXP) {
+            // a sum past 2^12, or no reference yet: raise it and take block j again
+            bool grow = false;
+#pragma unroll
+            for (int rb = 0; rb < RB; ++rb) grow = grow || sum[rb] > 4096.0f || m[rb] == -INFINITY;
+            if (__builtin_amdgcn_ballot_w64(grow) != 0) {
+#pragma unroll
+                for (int rb = 0; rb < RB; ++rb) {
+                    const f32x16& x = sc[PAR][rb];
+                    float top = x[0];
+#pragma unroll
+                    for (int r = 1; r < 16; ++r) top = fmaxf(top, x[r]);
+                    top *= a.scale_log2;
+                    const float up = fmaxf(m[rb], fmaxf(top, __shfl_xor(top, 32)));
+                    const float f = up == -INFINITY ? 1.0f : fast_exp2(m[rb] - up);
+                    m[rb] = up;
+                    l[rb] *= f;
+#pragma unroll
+                    for (int d = 0; d < ND; ++d)
+#pragma unroll
+                        for (int r = 0; r < 16; ++r) oacc[rb][d][r] *= f;
+                    const float nm = up == -INFINITY ? 0.0f : -up;
+                    sum[rb] = 0.0f;
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) {
+                        p[r] = fast_exp2(__builtin_fmaf(x[r], a.scale_log2, nm));
+                        sum[rb] += p[r];
+                        if (r % 8 == 7) weights8(rb, r & 8, p + (r & ~7));
+                    }
+                }
+            }
 #pragma unroll
             for (int rb = 0; rb < RB; ++rb) l[rb] += sum[rb];
+        }
     };
     static_assert(2 * ND == NKS, "as many V as K operands in a step");
 
@@ -506,33 +626,94 @@ void sdpa_prompt_wide_kernel(const PackArgs a) {
     constexpr std::integral_constant<int, 1> odd{};
     constexpr std::true_type on{};
     constexpr std::false_type off{};
-    // iteration t: K tile t and V tile t - 1 are staged; steps 2 t - 1 and 2 t
-    auto stage = [&](int t) SDPA_INLINE {
-        wait_vmem();
+    // iteration u of the group's tiles: K tile u and V tile u - 1 are staged;
+    // the second half of tile u - 1 and the first of tile u are taken
+    // the first tile with a key that some row of the workgroup does not keep
+    const int t_cut = (a.causal ? max(0, min(s.nk, q0 + s.coff + 1)) : s.nk) / TN;
+    bool again = false;
+    auto stage = [&](int u) SDPA_INLINE {
+        wait_copies<0>();
         __syncthreads();
-        if (t + 1 < ntiles) load_k(t + 1);
-        if (t < ntiles) load_v(t);
-    };
-    auto kt = [&](int t) SDPA_INLINE -> const uint8_t* { return smem + (t & 1) * C::TILEB; };
-    auto vt = [&](int t) SDPA_INLINE -> const uint8_t* { return smem + (2 + ((t - 1) & 1)) * C::TILEB; };
-    if (ntiles > 0) load_k(0);
-    int t = 0;
-    if (t_end > 0) {
-        stage(0);
-        step(odd, off, on, off, false, -1, kt(0), vt(0));
-        step(even, on, on, off, t_full == 0, 0, kt(0), vt(0));
-        for (t = 1; t < t_end; ++t) {
-            stage(t);
-            step(odd, on, on, on, t > t_full, 2 * t - 1, kt(t), vt(t));
-            step(even, on, on, on, t >= t_full, 2 * t, kt(t), vt(t));
+        if (again) {  // V tile u - 1, wherever some row of the workgroup does not keep all of it
+            if (u > 0 && tile(u - 1) >= t_cut && tile(u - 1) < ntiles)
+                clean_tile<T, C::TILEB>(buf + (2 + ((u - 1) & 1)) * C::TILEB, threadIdx.x & 255);
+            __syncthreads();
         }
-        stage(t);
-        step(odd, on, off, on, t > t_full, 2 * t - 1, kt(t), vt(t));
-        step(even, off, off, on, false, 2 * t, kt(t), vt(t));
-        ++t;
+        if (tile(u + 1) < ntiles) load_k(u + 1);
+        if (tile(u) < ntiles) load_v(u);
+    };
+    auto kt = [&](int u) SDPA_INLINE -> const uint8_t* { return buf + (u & 1) * C::TILEB; };
+    auto vt = [&](int u) SDPA_INLINE -> const uint8_t* { return buf + (2 + ((u - 1) & 1)) * C::TILEB; };
+    const int u_all = (ntiles + NG - 1) / NG;                               // iterations of the longest group
+    const int u_end = NG == 1 ? t_end : t_end > grp ? (t_end - grp + NG - 1) / NG : 0;  // this wave's tiles
+    for (;;) {
+#pragma unroll
+        for (int rb = 0; rb < RB; ++rb) {
+            m[rb] = -INFINITY;
+            l[rb] = 0.0f;
+#pragma unroll
+            for (int d = 0; d < ND; ++d) oacc[rb][d] = f32x16{};
+        }
+        if (tile(0) < ntiles) load_k(0);
+        int u = 0;
+        if (u_end > 0) {
+            stage(0);
+            step(odd, off, on, off, false, -1, kt(0), vt(0));
+            step(even, on, on, off, tile(0) >= t_full, 2 * tile(0), kt(0), vt(0));
+            for (u = 1; u < u_end; ++u) {
+                stage(u);
+                step(odd, on, on, on, tile(u - 1) >= t_full, 2 * tile(u - 1) + 1, kt(u), vt(u));
+                step(even, on, on, on, tile(u) >= t_full, 2 * tile(u), kt(u), vt(u));
+            }
+            stage(u);
+            step(odd, on, off, on, tile(u - 1) >= t_full, 2 * tile(u - 1) + 1, kt(u), vt(u));
+            step(even, off, off, on, false, 0, kt(u), vt(u));
+            ++u;
+        }
+        for (; u <= u_all; ++u) stage(u);
+        if (again || t_cut >= ntiles) break;
+        bool ok = true;
+#pragma unroll
+        for (int rb = 0; rb < RB; ++rb) ok = ok && all_finite<ND>(oacc[rb]);
+        again = __syncthreads_or(!ok) != 0;
+        if (!again) break;
     }
-    for (; t <= ntiles; ++t) stage(t);
 
+    if constexpr (NG > 1) {  // the second group's sums, then the first's join them
+        float* const js = reinterpret_cast<float*>(smem) + wave * RB * ND * 16 * 64 + lane;
+        __syncthreads();
+        if (grp == 1) {
+#pragma unroll
+            for (int rb = 0; rb < RB; ++rb) {
+                ml_s[(wave * RB + rb) * 64 + lane] = make_float2(m[rb], l[rb]);
+#pragma unroll
+                for (int d = 0; d < ND; ++d)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) js[((rb * ND + d) * 16 + r) * 64] = oacc[rb][d][r];
+            }
+        }
+        __syncthreads();
+        if (grp == 1) return;
+#pragma unroll
+        for (int rb = 0; rb < RB; ++rb) {
+            const float2 o = ml_s[(wave * RB + rb) * 64 + lane];
+            const float up = fmaxf(m[rb], o.x);
+            const float f0 = m[rb] == -INFINITY ? 0.0f : fast_exp2(m[rb] - up), f1 = o.x == -INFINITY ? 0.0f : fast_exp2(o.x - up);
+            m[rb] = up;
+            l[rb] = l[rb] * f0 + o.y * f1;
+#pragma unroll
+            for (int d = 0; d < ND; ++d)
+#pragma unroll
+                for (int r = 0; r < 16; ++r)
+                    oacc[rb][d][r] = oacc[rb][d][r] * f0 + js[((rb * ND + d) * 16 + r) * 64] * f1;
+        }
+    }
+    if (again) {
+        const rsrc_t vr = make_rsrc(static_cast<const T*>(a.v) + s.k0 * a.v_s[1] + hk * a.v_s[0], a.v_ext);
+#pragma unroll
+        for (int rb = 0; rb < RB; ++rb)
+            add_kept<T, ND>(vr, vrow, t_cut * TN, kend, a.causal ? qw + 32 * rb + n + s.coff : s.nk - 1, hf, oacc[rb]);
+    }
 #pragma unroll
     for (int rb = 0; rb < RB; ++rb) {
         const int qi = qw + 32 * rb + n;
@@ -559,24 +740,22 @@ void sdpa_prompt_wide_kernel(const PackArgs a) {
 
 template <typename T>
 static int launch_prompt_t(int D, const PackArgs& a, hipStream_t s) {
-    const dim3 grid((uint32_t)a.B * a.Hq * a.n_blk), block(256);
-    if constexpr (sizeof(T) == 2) {
-        if (a.wide) {
-            switch (D) {
-                case 32: sdpa_prompt_wide_kernel<T, 32><<<grid, block, 0, s>>>(a); break;
-                case 64: sdpa_prompt_wide_kernel<T, 64><<<grid, block, 0, s>>>(a); break;
-                case 128: sdpa_prompt_wide_kernel<T, 128><<<grid, block, 0, s>>>(a); break;
-                default: return (int)hipErrorInvalidValue;
-            }
-            return (int)hipGetLastError();
-        }
+    const dim3 grid((uint32_t)a.B * a.Hq * a.n_blk);
+#define SDPA_PROMPT_D(KERNEL, THREADS, ...)                                            \
+    switch (D) {                                                                       \
+        case 32: KERNEL<T, 32, ##__VA_ARGS__><<<grid, THREADS, 0, s>>>(a); break;      \
+        case 64: KERNEL<T, 64, ##__VA_ARGS__><<<grid, THREADS, 0, s>>>(a); break;      \
+        case 128: KERNEL<T, 128, ##__VA_ARGS__><<<grid, THREADS, 0, s>>>(a); break;    \
+        default: return (int)hipErrorInvalidValue;                                     \
     }
-    switch (D) {
-        case 32: sdpa_prompt_kernel<T, 32><<<grid, block, 0, s>>>(a); break;
-        case 64: sdpa_prompt_kernel<T, 64><<<grid, block, 0, s>>>(a); break;
-        case 128: sdpa_prompt_kernel<T, 128><<<grid, block, 0, s>>>(a); break;
-        default: return (int)hipErrorInvalidValue;
+    if constexpr (sizeof(T) == 4) {
+        SDPA_PROMPT_D(sdpa_prompt_kernel, 256)
+    } else if (a.groups == 2) {
+        SDPA_PROMPT_D(sdpa_prompt_wide_kernel, 512, 2)
+    } else {
+        SDPA_PROMPT_D(sdpa_prompt_wide_kernel, 256, 1)
     }
+#undef SDPA_PROMPT_D
     return (int)hipGetLastError();
 }
 
@@ -592,21 +771,29 @@ int launch_prompt(int dtype, int D, const PackArgs& a, void* stream) {
 // ------------------------------------------------------------------ key weights
 //
 // W[b, h', j] = sum over the query heads h of key head h' and the rows i that
-// keep key j of exp(s_hij - LSE_hi). A workgroup holds 256 keys in registers
-// (64 per wave) and runs over a range of one query head's rows, 64 at a time
+// keep key j of exp(s_hij - LSE_hi). A workgroup holds 128 keys in registers
+// (32 per wave) and runs over a range of one query head's rows, 64 at a time
 // through LDS: S = Q K^T puts one key in each lane's column, so the sum over
 // rows is lane-local. Rows whose LSE is -inf keep no key and add nothing.
+//
+// The exponentials bound it (16 of them a lane, with a multiply-add and an
+// addition each, to D / 16 products: 549 cycles of the vector unit for 32 rows
+// by 64 keys, measured, to 272 of the matrix unit at D = 64), so it runs four
+// waves a SIMD with little state, whose products and exponentials overlap
+// between waves. 2048 + 1531 tokens, 16 heads of 128: 34 us, against 44 with 64
+// keys a wave (two waves a SIMD) and 38 interleaved by hand as the prompt
+// kernel.
 template <typename T, int D>
-__global__ __attribute__((amdgpu_flat_work_group_size(256, 256), amdgpu_waves_per_eu(2)))
+__global__ __attribute__((amdgpu_flat_work_group_size(256, 256), amdgpu_waves_per_eu(4)))
 void sdpa_key_weight_kernel(const PackArgs a) {
-    constexpr int NW = 4, TN = sizeof(T) == 2 ? 64 : 32, KB = sizeof(T) == 2 ? 2 : 1;
+    constexpr int NW = 4, TN = sizeof(T) == 2 ? 64 : 32;
     using C = TwoPassCfg<T, D, NW, MASK_NONE, true, TN, true>;
     using TR = Tr<T>;
     using vec = typename TR::vec;
     constexpr int SZ = (int)sizeof(T), NQB = TN / 32, KSTEP = 2 * TR::KH, NKS = D / KSTEP;
-    constexpr int BLK = 32 * KB * NW;
     __shared__ __attribute__((aligned(16))) uint8_t smem[2 * C::TILEB];
-    __shared__ float lse_s[2][TN];
+    __shared__ __attribute__((aligned(16))) float lse_s[2][TN];
+    __shared__ int odd_s[2];  // a row of the tile has an infinite LSE
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 31, hf = lane >> 5;
@@ -614,7 +801,7 @@ void sdpa_key_weight_kernel(const PackArgs a) {
     const PackWork w = pack_work(blockIdx.x, a.B, per, a.n_blk);
     const int h = w.h / a.n_split, split = w.h - h * a.n_split;
     const Seq s = sequence(a, w.b);
-    const int k0 = w.blk * BLK;  // causal: low keys are the heaviest
+    const int k0 = w.blk * KEY_WEIGHT_KEYS;  // causal: low keys are the heaviest
     if (k0 >= s.nk) return;
     const int hk = h / a.group;
     // rows of this range; the first row that keeps a key of the block
@@ -622,101 +809,105 @@ void sdpa_key_weight_kernel(const PackArgs a) {
     const int r1 = min(s.nq, r0 + a.split_rows);
     if (a.causal) r0 = max(r0, (k0 - s.coff) / TN * TN);
     const int ntiles = r1 > r0 ? (r1 - r0 + TN - 1) / TN : 0;
+    const int kw = k0 + wave * 32;
+    float* const ws = a.ws + (((int64_t)(h % a.group * a.n_split + split) * a.B + w.b) * a.Hkv + hk) * a.max_k;
 
-    const rsrc_t qr = make_rsrc(static_cast<const T*>(a.q) + s.q0 * a.q_s[1] + h * a.q_s[0], a.q_ext);
+    const desc_t qd = make_desc(static_cast<const T*>(a.q) + s.q0 * a.q_s[1] + h * a.q_s[0], a.q_ext);
     const rsrc_t kr = make_rsrc(static_cast<const T*>(a.k) + s.k0 * a.k_s[1] + hk * a.k_s[0], a.k_ext);
     const rsrc_t lr = make_rsrc(a.lse + s.q0 * a.l_s[1] + h * a.l_s[0], a.l_ext);
     const uint32_t qrow = (uint32_t)(a.q_s[1] * SZ);
-
-    const int kw = k0 + wave * 32 * KB;
-    vec kf[KB][NKS];
-#pragma unroll
-    for (int kb = 0; kb < KB; ++kb) {
-        const int key = kw + 32 * kb + n;
-        const bool ok = key < s.nk;
-        const uint32_t off = (uint32_t)((ok ? key : 0) * a.k_s[1] * SZ);
-#pragma unroll
-        for (int c = 0; c < NKS; ++c) kf[kb][c] = load_operand<T>(kr, pred(ok, off + (c * KSTEP + hf * TR::KH) * SZ), a.q_mul);
+    if (ntiles == 0) {  // no row of this range keeps a key of the block
+        for (int key = kw + lane; key < min(kw + 32, s.nk); key += 64) ws[key] = 0.0f;
+        return;
     }
-    auto load_tile = [&](int t) SDPA_INLINE {
-        uint8_t* const qd = smem + (t & 1) * C::TILEB;
+    vec kf[NKS];
+    {
+        const int key = kw + n;
+        const bool ok = key < s.nk;
+        const uint32_t row = (uint32_t)((ok ? key : 0) * a.k_s[1] * SZ);
+        uint32_t off[NKS];
+#pragma unroll
+        for (int c = 0; c < NKS; ++c) off[c] = pred(ok, row + (c * KSTEP + hf * TR::KH) * SZ);
+        load_operands<T, NKS>(kr, off, a.q_mul, kf);
+    }
+    constexpr int LROWS = NW * C::RPI;
+    const int lrow = wave * C::RPI + lane / C::CPR;
+    const uint32_t qvo = lrow * qrow;
+    constexpr bool SAME = C::fk(LROWS) == 0;  // the chunk order repeats from one load to the next
+    const uint32_t lds = lds_address(smem);
+    auto load_q = [&](int t) SDPA_INLINE {
+        const uint32_t dst = lds + (t & 1) * C::TILEB;
         const int base = r0 + t * TN;
 #pragma unroll
         for (int jj = 0; jj < C::NI / NW; ++jj) {
-            const int j = jj * NW + wave;
-            const int row = j * C::RPI + lane / C::CPR;
-            const int cq = (lane % C::CPR) ^ C::fk(row);
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(qr, (lds_void*)(qd + j * 1024), 16,
-                                                     pred(base + row < r1, row * qrow + cq * 16), (uint32_t)base * qrow, 0, 0);
+            const uint32_t c = ((lane % C::CPR) ^ C::fk(SAME ? lrow : lrow + jj * LROWS)) * 16;
+            copy_to_lds(qd, dst + (jj * NW + wave) * 1024,
+                        pred(base + jj * LROWS + lrow < r1, qvo + c + (uint32_t)(base + jj * LROWS) * qrow));
         }
     };
-    // -LSE in base 2 of a tile's rows; rows past the range and dead rows -inf
+    // -LSE in base 2 of a tile's rows (the first wave); rows past the range and rows without keys: -inf
     auto load_lse = [&](int t) SDPA_INLINE -> float {
-        const int row = r0 + t * TN + (int)threadIdx.x;
-        const bool ok = (int)threadIdx.x < TN && row < r1;
+        const int row = r0 + t * TN + lane;
+        const bool ok = lane < TN && row < r1;
         const float x = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(
                                                       lr, pred(ok, (uint32_t)((ok ? row : 0) * a.l_s[1] * 4)), 0, 0));
-        return ok && x != -INFINITY ? -x * LOG2E : -INFINITY;
+        return ok ? x : -INFINITY;
     };
-    float sum[KB];
-#pragma unroll
-    for (int kb = 0; kb < KB; ++kb) sum[kb] = 0.0f;
-    auto tile = [&](int t, auto edge_c) SDPA_INLINE {
-        constexpr bool edge = decltype(edge_c)::value;
+    auto store_lse = [&](int t, float x) SDPA_INLINE {
+        const int row = r0 + t * TN + lane;
+        const bool inf = fabsf(x) == INFINITY;
+        if (lane < TN) lse_s[t & 1][lane] = inf ? -INFINITY : -x * LOG2E;
+        const bool odd = __builtin_amdgcn_ballot_w64(lane < TN && row < r1 && inf) != 0;
+        if (lane == 0) odd_s[t & 1] = odd;
+    };
+    const int kr0 = swap23(n);
+    float sum = 0.0f;
+    // the tile's rows, 32 at a time
+    auto tile = [&](int t) SDPA_INLINE {
         const uint8_t* const qt = smem + (t & 1) * C::TILEB;
 #pragma unroll
         for (int qb = 0; qb < NQB; ++qb) {
-            f32x16 acc[KB];
-#pragma unroll
-            for (int kb = 0; kb < KB; ++kb) acc[kb] = f32x16{};
-#pragma unroll
-            for (int c = 0; c < NKS; ++c) {
-                const int row = 32 * qb + swap23(n), elem = c * KSTEP + hf * TR::KH;
-                const vec qa = *reinterpret_cast<const vec*>(qt + C::pos_k(row, elem * SZ / 16) * 16 + ((elem * SZ) & 15));
-#pragma unroll
-                for (int kb = 0; kb < KB; ++kb) acc[kb] = TR::mfma(qa, kf[kb][c], acc[kb]);
-            }
+            const float* const lp = lse_s[t & 1] + 32 * qb;
             float nl[16];
 #pragma unroll
-            for (int r = 0; r < 16; ++r) nl[r] = lse_s[t & 1][32 * qb + kk(hf, r)];
+            for (int r = 0; r < 16; ++r) nl[r] = lp[kk(hf, r)];
+            f32x16 acc = {};
 #pragma unroll
-            for (int kb = 0; kb < KB; ++kb) {
-                // row i keeps key j when j <= i + coff
-                const int lim = a.causal ? kw + 32 * kb + n - s.coff - (r0 + t * TN + 32 * qb) - 8 * hf : -64;
-#pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    float p = fast_exp2(__builtin_fmaf(acc[kb][r], a.scale_log2, nl[r]));
-                    if constexpr (edge) p = kk(0, r) < lim || nl[r] == -INFINITY ? 0.0f : p;
-                    sum[kb] += p;
-                }
+            for (int c = 0; c < NKS; ++c) {
+                const int row = 32 * qb + kr0, elem = c * KSTEP + hf * TR::KH;
+                const vec qa = *reinterpret_cast<const vec*>(qt + C::pos_k(row, elem * SZ / 16) * 16 + ((elem * SZ) & 15));
+                acc = TR::mfma(qa, kf[c], acc);
             }
+            const int i0 = r0 + t * TN + 32 * qb;  // the block's first row
+            if ((a.causal && i0 + s.coff < kw + 31) || odd_s[t & 1]) {
+                // row i keeps key j when j <= i + coff; rows of infinite LSE count for nothing
+                const int lim = a.causal ? kw + n - s.coff - i0 - 8 * hf : -64;
+#pragma unroll
+                for (int r = 0; r < 16; ++r) acc[r] = kk(0, r) < lim || nl[r] == -INFINITY ? -INFINITY : acc[r];
+            }
+            float x[2] = {0.0f, 0.0f};
+#pragma unroll
+            for (int r = 0; r < 16; ++r) x[r & 1] += fast_exp2(__builtin_fmaf(acc[r], a.scale_log2, nl[r]));
+            sum += x[0] + x[1];
         }
     };
-    if (ntiles > 0) {
-        load_tile(0);
-        const float x = load_lse(0);
-        if (threadIdx.x < TN) lse_s[0][threadIdx.x] = x;
-        wait_vmem();
-    }
-    __syncthreads();
+    // iteration t: row tile t and its LSE are staged
+    load_q(0);
+    float x = 0.0f;
+    if (wave == 0) x = load_lse(0);
     for (int t = 0; t < ntiles; ++t) {
-        float x = 0.0f;
-        if (t + 1 < ntiles) {
-            load_tile(t + 1);
-            x = load_lse(t + 1);
-        }
-        tile(t, std::true_type{});
-        wait_vmem();
-        if (t + 1 < ntiles && threadIdx.x < TN) lse_s[(t + 1) & 1][threadIdx.x] = x;
+        if (wave == 0) store_lse(t, x);
+        wait_copies<0>();
         __syncthreads();
+        if (t + 1 < ntiles) {
+            load_q(t + 1);
+            if (wave == 0) x = load_lse(t + 1);
+        }
+        tile(t);
     }
-#pragma unroll
-    for (int kb = 0; kb < KB; ++kb) {
-        const int key = kw + 32 * kb + n;
-        const float x = sum[kb] + __shfl_xor(sum[kb], 32);
-        if (hf == 0 && key < s.nk)
-            a.ws[(((int64_t)(h % a.group * a.n_split + split) * a.B + w.b) * a.Hkv + hk) * a.max_k + key] = x;
-    }
+    const int key = kw + n;
+    const float total = sum + __shfl_xor(sum, 32);
+    if (hf == 0 && key < s.nk) ws[key] = total;
 }
 
 // W = the ranges' sums in order; zeros past a sequence's keys
@@ -749,8 +940,6 @@ static int launch_key_weights_t(int D, const PackArgs& a, hipStream_t s) {
     sdpa_key_weight_sum_kernel<<<dim3((a.w_cols + 255) / 256, a.B * a.Hkv), block, 0, s>>>(a);
     return (int)hipGetLastError();
 }
-
-int key_weight_block(int dtype) { return dtype == DT_F32 ? 128 : 256; }
 
 int launch_key_weights(int dtype, int D, const PackArgs& a, void* stream) {
     hipStream_t s = static_cast<hipStream_t>(stream);

@@ -29,7 +29,7 @@ struct PackArgs {
     int o_vec;            // rows of O take aligned 16-byte stores
     int q_mul;            // 1, or the factor -1 or 0 that the queries are taken with
     float scale_log2;     // |scale| * log2(e) (1 when the scale is 0)
-    int wide;             // prompt: the kernel of 256 rows a workgroup
+    int groups;           // prompt: wave groups of the 16-bit kernel (1 or 2)
     int n_blk;            // blocks per (sequence, head)
     int n_split;          // key weights: query ranges per key block and query head
     int split_rows;       // key weights: queries of a range
@@ -37,13 +37,9 @@ struct PackArgs {
     uint32_t q_ext, k_ext, v_ext, o_ext, l_ext;  // byte extents of one (sequence, head) slice
 };
 
-// Query rows of one workgroup of the prompt kernels.
-#ifndef WIDE_RB
-#define WIDE_RB 1
-#endif
-constexpr int PROMPT_ROWS = 128, PROMPT_WIDE_ROWS = 128 * WIDE_RB;
+constexpr int PROMPT_ROWS = 128;  // query rows of one workgroup of the prompt kernels
 int launch_prompt(int dtype, int D, const PackArgs& a, void* stream);
-int key_weight_block(int dtype);  // keys of one workgroup
+constexpr int KEY_WEIGHT_KEYS = 128;  // keys of one workgroup of the key-weight kernel
 int launch_key_weights(int dtype, int D, const PackArgs& a, void* stream);
 
 // The paged 8-bit cache. k [n_pages, Hkv, page, D] and v [n_pages, Hkv, D, page]

@@ -6,7 +6,6 @@
 
 #include <algorithm>
 #include <cmath>
-#include <cstdlib>
 #include <cstring>
 
 #include "api_checks.h"
@@ -120,22 +119,27 @@ sdpa_status_t grid_ok(int64_t n) {
     return SDPA_OK;
 }
 
-// Prompt attention: the kernel of 256 rows a workgroup for 16-bit types,
-// where its blocks still give every CU one.
-bool prompt_wide(const sdpa::PackArgs& a, int dtype) {
-    if (dtype == SDPA_F32) return false;
-    if (const char* e = std::getenv("SDPA_WIDE")) return e[0] == '1';
-    return (int64_t)a.B * a.Hq * cdiv(a.max_q, sdpa::PROMPT_WIDE_ROWS) >= 256;
+// Prompt attention: two groups of four waves a workgroup, each on every other
+// key tile, where one group a block leaves wave slots empty (512 workgroups of
+// four waves fill two slots of every SIMD) and the chain of tiles is long
+// enough to pay for joining the groups. Measured, one group and two: 4096
+// tokens x 16 heads of 128 (512 blocks) 91 and 86 us, 1024 x 4 and less ragged
+// ones x 8 heads of 64 (320 blocks) 17.3 and 15.9; 2048 x 4 x 16 heads of 64
+// (1024 blocks) 50 and 61, 512 and 300 tokens x 16 heads 13.7 and 14.3.
+int prompt_groups(const sdpa::PackArgs& a) {
+    const int64_t blocks = (int64_t)a.B * a.Hq * cdiv(a.max_q, sdpa::PROMPT_ROWS);
+    return blocks <= 512 && a.max_k >= 768 ? 2 : 1;
 }
 
-// Key weights: ranges of one query head's rows. A key block's work is a range
-// of rows; ranges are added until the grid holds four workgroups for each of
-// the 256 CUs (the triangle of a causal call needs several rounds to balance),
-// none below 512 rows.
-void plan_key_weights(sdpa::PackArgs* a, int dtype) {
-    a->n_blk = (int)cdiv(a->max_k, sdpa::key_weight_block(dtype));
+// Key weights: ranges of one query head's rows, enough for 2048 workgroups
+// (two rounds of the 1024 resident ones: the triangle of a causal call needs
+// them to balance), none below 256 rows. Measured with 1024, 2048 and 4096
+// workgroups: 2048 + 1531 tokens x 16 heads of 128 38.7, 32.1 and 36.7 us,
+// 8191 tokens x 16 heads of 64 136, 120 and 128 us.
+void plan_key_weights(sdpa::PackArgs* a) {
+    a->n_blk = (int)cdiv(a->max_k, sdpa::KEY_WEIGHT_KEYS);
     const int64_t blocks = std::max<int64_t>(1, (int64_t)a->B * a->Hq * a->n_blk);
-    const int64_t want = std::min<int64_t>(cdiv(1024, blocks), std::max<int64_t>(1, a->max_q / 512));
+    const int64_t want = std::min<int64_t>(cdiv(2048, blocks), std::max<int64_t>(1, a->max_q / 256));
     a->split_rows = (int)std::max<int64_t>(64, cdiv(cdiv(a->max_q, want), 64) * 64);
     a->n_split = (int)std::max<int64_t>(1, cdiv(a->max_q, a->split_rows));
 }
@@ -318,8 +322,8 @@ sdpa_status_t sdpa_prompt_fwd(const sdpa_tensor_t* q, const sdpa_tensor_t* k, co
     TRY(pack_extent(out, "out", a.max_q, out->sizes[2], &a.o_ext));
     TRY(pack_extent(lse, "lse", a.max_q, 1, &a.l_ext));
     const int D = (int)q->sizes[2];
-    a.wide = prompt_wide(a, q->dtype);
-    a.n_blk = (int)cdiv(a.max_q, a.wide ? sdpa::PROMPT_WIDE_ROWS : sdpa::PROMPT_ROWS);
+    a.groups = prompt_groups(a);
+    a.n_blk = (int)cdiv(a.max_q, sdpa::PROMPT_ROWS);
     TRY(grid_ok(n_seqs * a.Hq * a.n_blk));
     return launched(sdpa::launch_prompt(q->dtype, D, a, hip_stream));
 }
@@ -331,7 +335,7 @@ sdpa_status_t sdpa_key_weights_workspace_bytes(const sdpa_tensor_t* q, const sdp
     *bytes = 0;
     sdpa::PackArgs a;
     TRY(pack_args(q, k, n_seqs, max_q, max_k, enable_gqa, &a));
-    plan_key_weights(&a, q->dtype);
+    plan_key_weights(&a);
     *bytes = (size_t)key_weight_ws(a);
     return SDPA_OK;
 }
@@ -348,7 +352,7 @@ sdpa_status_t sdpa_key_weights(const sdpa_tensor_t* q, const sdpa_tensor_t* k, c
     const int64_t want[3] = {n_seqs, a.Hkv, max_k};
     TRY(check_f32(weights, "weights", 3, want));
     TRY(split_scale(scale, &a.scale_log2, &a.q_mul));
-    plan_key_weights(&a, q->dtype);
+    plan_key_weights(&a);
     if (n_seqs == 0 || max_k == 0) return SDPA_OK;
     const int64_t need = key_weight_ws(a);
     if (need > 0 && (!workspace || workspace_bytes < (size_t)need || reinterpret_cast<uintptr_t>(workspace) % 16))

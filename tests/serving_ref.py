@@ -56,6 +56,15 @@ def limits(n_q, n_k, causal, align):
     return i + (n_k - n_q if align == "bottom_right" else 0)
 
 
+def odd_values(kept, v):
+    """What the values that are not finite add to each row that keeps their key (0 elsewhere)."""
+    x = torch.where(torch.isfinite(v), torch.zeros_like(v), v)
+    j = (x != 0).any(1).nonzero()[:, 0]
+    if not len(j):
+        return torch.zeros(kept.shape[0], v.shape[1], dtype=torch.float64)
+    return torch.where(kept[:, j, None], x[None, j], torch.zeros_like(x[None, j])).sum(1)
+
+
 def prompt(q, k, v, cu_q, cu_k, causal=True, align="top_left", scale=None):
     """(O, LSE, bound of O, bound of LSE) of packed sequences; NaN at tokens of no sequence."""
     Tq, Hq, D = q.shape
@@ -73,14 +82,15 @@ def prompt(q, k, v, cu_q, cu_k, causal=True, align="top_left", scale=None):
             p, L = softmax(s)
             vv = v[c:e, h // g].double()
             kept = torch.where(p > 0, p, torch.zeros_like(p))
-            o[a:z, h] = kept @ torch.nan_to_num(vv, 0.0, 0.0, 0.0)
+            o[a:z, h] = kept @ torch.nan_to_num(vv, 0.0, 0.0, 0.0) + odd_values(s > -math.inf, vv)
             A = kept @ torch.nan_to_num(vv.abs(), 0.0, 0.0, 0.0)
             sl = rel_slack(S, D, e - c)
             lse[a:z, h] = L
-            to[a:z, h] = u(q.dtype) * o[a:z, h].abs() + ((up + sl) * (1 + u(q.dtype)))[:, None] * A + 1e-30
+            to[a:z, h] = u(q.dtype) * torch.nan_to_num(o[a:z, h], 0.0, 0.0, 0.0).abs() + ((up + sl) * (1 + u(q.dtype)))[:, None] * A + 1e-30
             if q.dtype == torch.float16:
-                # fp16 probabilities below 2^-14 and results near 0 round to steps of 2^-24; the row sum is at least 1
-                to[a:z, h] += 2.0 ** -25 * (1 + (p > 0).double() @ torch.nan_to_num(vv.abs(), 0.0, 0.0, 0.0))
+                # fp16 probabilities below 2^-14 and results near 0 round to steps of 2^-24; a row's largest
+                # probability is taken as 1/2 at least (its reference is rounded up to a whole power of two)
+                to[a:z, h] += 2.0 ** -25 * (1 + 2 * (p > 0).double() @ torch.nan_to_num(vv.abs(), 0.0, 0.0, 0.0))
             tl[a:z, h] = sl + 2.0 ** -22 * torch.nan_to_num(L, 0.0, 0.0, 0.0).abs()
     return o, lse, to, tl
 
@@ -212,12 +222,12 @@ def attention(q, cache, table, lens, cu, causal=True, scale=None, w=None, max_kv
             s = s.masked_fill(~ok[None, :], -math.inf)
             p, l = softmax(s)
             vz = torch.nan_to_num(v, 0.0, 0.0, 0.0)
-            o[a:z, h] = p @ vz
+            o[a:z, h] = p @ vz + odd_values(s > -math.inf, v)
             A = p @ vz.abs()
             sl = rel_slack(torch.nan_to_num(S, 0.0), D, L)
             lse[a:z, h] = l
             # probabilities as a bf16 rounding plus its bf16 residual: 2^-8 * 2^-8
-            to[a:z, h] = u(q.dtype) * o[a:z, h].abs() + ((2.0 ** -16 + sl) * (1 + u(q.dtype)))[:, None] * A + 1e-30
+            to[a:z, h] = u(q.dtype) * torch.nan_to_num(o[a:z, h], 0.0, 0.0, 0.0).abs() + ((2.0 ** -16 + sl) * (1 + u(q.dtype)))[:, None] * A + 1e-30
             if q.dtype == torch.float16:
                 to[a:z, h] += 2.0 ** -25  # half of fp16's smallest step
             tl[a:z, h] = sl + 2.0 ** -22 * torch.nan_to_num(l, 0.0, 0.0, 0.0).abs()

@@ -97,6 +97,28 @@ def test_prompt_and_weights(case):
     _near(label + " weights", got, W, bound)
 
 
+@pytest.mark.parametrize("dt,D,n", [("bf16", 128, 300), ("f16", 64, 130), ("f32", 32, 100), ("bf16", 32, 900),
+                                    ("f16", 128, 1000), ("f32", 128, 70)])
+def test_prompt_values_that_are_not_finite(dt, D, n):
+    """NaN and infinities in keys and values reach the rows that keep them, and no other."""
+    S = _lib()
+    q, k, v, cq, ck = _packed(n + D, [n, 50], [n, 50], 4, 2, D, TD[dt])
+    v[n // 2, 0, 3] = float("nan")
+    v[n // 3, 1, 5] = float("inf")
+    v[n // 3 + 7, 1, 5] = -float("inf")
+    v[n - 2, 1, D - 1] = -float("inf")
+    v[n + 49, 0, 1] = float("nan")
+    k[n - 5, 0, 2] = float("nan")  # its scores are NaN for the rows that keep it
+    o, lse, to, tl = R.prompt(q, k, v, cq, ck)
+    O, L = S.prompt_attention(*[x.to(DEV) for x in (q, k, v, cq, ck)], n, n, enable_gqa=True)
+    torch.cuda.synchronize()
+    bad = torch.zeros(n + 50, 4, dtype=torch.bool)
+    bad[n - 5:n, :2] = True  # rows of the key head with the NaN key
+    assert torch.isnan(L.cpu()[bad]).all() and torch.isnan(O.cpu()[bad]).all()
+    _near("O", O.cpu()[~bad], o[~bad], to[~bad])
+    _near("LSE", L.cpu()[~bad], lse[~bad], tl[~bad])
+
+
 def _fill(g, n_pages, H, P, D):
     k = (torch.randn(n_pages, H, P, D, generator=g) * 130).clamp(-448, 448).to(torch.float8_e4m3fn)
     v = (torch.randn(n_pages, H, D, P, generator=g) * 130).clamp(-448, 448).to(torch.float8_e4m3fn)
@@ -231,6 +253,28 @@ def test_cache_attention(case):
         S.cache_attention(q.to(DEV), c, table.to(DEV), il.to(DEV), cu.to(DEV), max(new), max_kv, is_causal=causal,
                           scale=scale, enable_gqa=Hq != H, weights=again)
         assert torch.equal(again, kw["weights_out"])
+
+
+@pytest.mark.parametrize("n,D,P,dt", [(8, 128, 64, "bf16"), (5, 64, 16, "f16"), (3, 32, 32, "bf16")])
+def test_cache_attention_codes_that_are_not_finite(n, D, P, dt):
+    """NaN codes reach the rows that keep their tokens, and no other."""
+    S = _lib()
+    H, g = 2, _gen(n + D)
+    lens, new = [100, 64], [n, n]
+    counts = [-(-x // P) for x in lens]
+    cache = _fill(g, sum(counts), H, P, D)
+    table, _ = _table(g, counts, sum(counts))
+    for b, j, h, d in ((0, 99, 0, 3), (0, 98, 1, D - 1), (0, 20, 1, 4), (1, 62, 0, 0)):
+        cache[1].view(torch.uint8)[int(table[b, j // P]), h, d, j % P] = R.NAN8 | (128 if d == 4 else 0)
+    il, cu = torch.tensor(lens, dtype=torch.int32), _cu(new)
+    q = torch.randn(2 * n, 4, D, generator=g).to(TD[dt])
+    o, lse, to, tl, _, _ = R.attention(q, cache, table, il, cu)
+    c = S.PagedCache(*[x.to(DEV) for x in cache])
+    O, L = S.cache_attention(q.to(DEV), c, table.to(DEV), il.to(DEV), cu.to(DEV), n, enable_gqa=True)
+    torch.cuda.synchronize()
+    assert torch.isnan(o).any() and not torch.isnan(o).all()
+    _near("O", O, o, to)
+    _near("LSE", L, lse, tl)
 
 
 def test_cache_attention_pages_past_the_pool():
