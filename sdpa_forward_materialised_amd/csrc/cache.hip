@@ -57,120 +57,204 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t c, float ratio) {
     return encode2(x[0] * ratio, x[1] * ratio) | encode2(x[2] * ratio, x[3] * ratio) << 16;
 }
 
-template <typename T>
-__device__ __forceinline__ void load8(const T* p, float* x) {
-    const u32x4 v = *reinterpret_cast<const u32x4*>(p);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = Tr<T>::to_f((v[e >> 1] >> (16 * (e & 1))) & 0xffffu);
-}
-
 __device__ __forceinline__ int held_tokens(const CacheArgs& a, int b) {
     return (int)min((int64_t)max(a.lens[b], 0), (int64_t)a.max_pages * a.page);
 }
 
 // ----------------------------------------------------------------------- append
 //
-// One workgroup per (page, key head) and per k or v: the new tokens' largest
-// magnitude gives the scale they need; a page that already holds tokens keeps
-// the larger of that and its own scale, its codes re-rounded when it grows.
-// Reads 2 bytes and writes 1 per element: bound by HBM, and by latency for
-// single tokens.
-template <typename T>
-__global__ __attribute__((amdgpu_flat_work_group_size(256, 256)))
-void sdpa_cache_append_kernel(const CacheArgs a) {
-    __shared__ float red[4];
-    __shared__ __attribute__((aligned(16))) uint8_t tr[128 * (128 + 4)];  // v codes [D][page + 4]
-    const int tid = threadIdx.x;
-    int id = blockIdx.x;
-    const int is_v = id & 1;
-    id >>= 1;
-    const int h = id % a.Hkv;
-    id /= a.Hkv;
-    const int slot = id % a.slots, b = id / a.slots;
-    const int c0 = min(max(a.cu[b], 0), a.T);
-    const int held = held_tokens(a, b);
-    const int count = (int)min((int64_t)min(min(max(a.cu[b + 1], c0), a.T) - c0, a.max_new),
-                               (int64_t)a.max_pages * a.page - held);
-    const int pi = (held >> a.page_log2) + slot;
-    const int lo = max(held, pi * a.page), hi = min(held + count, (pi + 1) * a.page);
-    if (lo >= hi) return;
-    const int page = a.table[b * a.table_s + pi];
-    if (page < 0 || page >= a.n_pages) return;
-    const int off = lo - pi * a.page, n = hi - lo;
-    const int ch = a.D / 8;  // 8-element chunks of a token
-    const int64_t* st = is_v ? a.nv_s : a.nk_s;
-    const T* src = static_cast<const T*>(is_v ? a.nv : a.nk) + h * st[0] + (int64_t)(c0 + lo - held) * st[1];
-    float* const scale = (is_v ? a.vs : a.ks) + (int64_t)page * a.Hkv + h;
-    uint8_t* const dst = (is_v ? a.v : a.k) + ((int64_t)page * a.Hkv + h) * a.page * a.D;
-
-    float amax = 0.0f;
-    for (int i = tid; i < n * ch; i += 256) {
-        float x[8];
-        load8(src + (i / ch) * st[1] + (i % ch) * 8, x);
+// One wave per (page, key head), the page's new keys and values in its
+// registers: for each of the two, the largest magnitude gives the scale they
+// need; a page that already holds tokens keeps the larger of that and its own
+// scale, its codes re-rounded when it grows. A lane takes 8 head-dim columns of
+// 4 consecutive tokens, so that both layouts are written without a pass through
+// LDS: k as 8 codes of a token, v as 4 tokens of a column. Reads 2 bytes and
+// writes 1 per element; the chain lengths -> table -> elements -> scale of
+// dependent loads bounds it, which k and v go through together.
+template <int D, int P, bool V>
+__device__ __forceinline__ void rescale_held(uint8_t* dst, int off, float ratio, int lane) {
+    // words of 4 codes: k, those of the tokens before `off`; v, of their 4
+    // slots those before `off`
+    constexpr int ROW = V ? P / 4 : D / 4;
+    const int n = V ? D * ROW : off * ROW;
+    for (int i0 = lane; i0 < n; i0 += 8 * 64) {
+        uint32_t w[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) amax = fmaxf(amax, finite(x[e]) ? fabsf(x[e]) : 0.0f);
-    }
-#pragma unroll
-    for (int k = 1; k < 64; k *= 2) amax = fmaxf(amax, __shfl_xor(amax, k));
-    if ((tid & 63) == 0) red[tid >> 6] = amax;
-    const float was = off > 0 ? *scale : 0.0f;
-    __syncthreads();  // every thread has read the old scale
-    amax = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
-    const float now = fmaxf(scale_for(amax), was);
-    const float inv = inverse(now);
-    if (tid == 0) *scale = now;
-    if (off > 0 && now > was) {  // the held codes move to the larger scale
-        const float ratio = was * inv;
-        if (!is_v) {
-            for (int i = tid; i < off * a.D / 4; i += 256) {
-                uint32_t* p = reinterpret_cast<uint32_t*>(dst) + i;
-                *p = rescale4(*p, ratio);
-            }
-        } else {
-            for (int i = tid; i < off * a.D; i += 256) {
-                uint8_t* p = dst + (i / off) * a.page + i % off;
-                *p = (uint8_t)rescale4(*p, ratio);
-            }
+        for (int k = 0; k < 8; ++k) {
+            const int i = i0 + 64 * k;
+            w[k] = i < n && (!V || 4 * (i % ROW) < off) ? reinterpret_cast<const uint32_t*>(dst)[i] : 0u;
         }
-    }
-    const int pitch = a.page + 4;
-    for (int i = tid; i < n * ch; i += 256) {
-        const int t = i / ch, c = i % ch;
-        float x[8];
-        load8(src + t * st[1] + c * 8, x);
-        u32x2 code;
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
-            code[e] = encode2(x[4 * e] * inv, x[4 * e + 1] * inv) | encode2(x[4 * e + 2] * inv, x[4 * e + 3] * inv) << 16;
-        if (!is_v) {
-            *reinterpret_cast<u32x2*>(dst + (off + t) * a.D + c * 8) = code;
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) tr[(c * 8 + e) * pitch + t] = (uint8_t)(code[e >> 2] >> (8 * (e & 3)));
-        }
-    }
-    if (!is_v) return;
-    __syncthreads();
-    if (off == 0 && n == a.page) {  // a whole page: 4 tokens a store
-        const int per = a.page / 4;
-        for (int i = tid; i < a.D * per; i += 256) {
-            const int d = i / per, t = 4 * (i % per);
-            *reinterpret_cast<uint32_t*>(dst + d * a.page + t) = *reinterpret_cast<const uint32_t*>(tr + d * pitch + t);
-        }
-    } else {
-        for (int i = tid; i < a.D * n; i += 256) {
-            const int d = i / n, t = i % n;
-            dst[d * a.page + off + t] = tr[d * pitch + t];
+        for (int k = 0; k < 8; ++k) {
+            const int i = i0 + 64 * k, t = V ? 4 * (i % ROW) : 0;
+            if (i >= n || (V && t >= off)) continue;
+            const int m = V ? min(off - t, 4) : 4;
+            const uint32_t mask = m == 4 ? 0xffffffffu : (1u << (8 * m)) - 1u;
+            reinterpret_cast<uint32_t*>(dst)[i] = (rescale4(w[k], ratio) & mask) | (w[k] & ~mask);
         }
     }
 }
 
+template <typename T, int D, int P>
+__global__ __attribute__((amdgpu_flat_work_group_size(256, 256)))
+void sdpa_cache_append_kernel(const CacheArgs a) {
+    constexpr int LOG = P == 16 ? 4 : P == 32 ? 5 : P == 64 ? 6 : 7;
+    constexpr int CH = D / 8, NU = (P / 4 * CH + 63) / 64;  // units of 4 tokens, units of a lane at most
+    // up to 4 units of a lane stay in registers; of more, the second half is
+    // read again (from cache) when its codes are made
+    constexpr int KEEP = NU < 4 ? NU : 4;
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    int id = blockIdx.x * 4 + wave;
+    const int h = id % a.Hkv;
+    id /= a.Hkv;
+    const int slot = id % a.slots, b = id / a.slots;
+    if (b >= a.B) return;
+    const int c0 = min(max(a.cu[b], 0), a.T);
+    const int held = held_tokens(a, b);
+    const int count = (int)min((int64_t)min(min(max(a.cu[b + 1], c0), a.T) - c0, a.max_new),
+                               (int64_t)a.max_pages * P - held);
+    const int pi = (held >> LOG) + slot;
+    const int lo = max(held, pi * P), hi = min(held + count, (pi + 1) * P);
+    if (lo >= hi) return;
+    const int page = a.table[b * a.table_s + pi];
+    if (page < 0 || page >= a.n_pages) return;
+    const int off = lo - pi * P, end = hi - pi * P;  // the page's new slots
+    const int t_first = off & ~3, units = ((end - t_first + 3) >> 2) * CH;
+    const int64_t at = (int64_t)page * a.Hkv + h, tok0 = c0 + pi * P - held;
+    // element [slot][column] of the page's new tokens
+    const T* const src[2] = {static_cast<const T*>(a.nk) + h * a.nk_s[0] + tok0 * a.nk_s[1],
+                             static_cast<const T*>(a.nv) + h * a.nv_s[0] + tok0 * a.nv_s[1]};
+    const int64_t row[2] = {a.nk_s[1], a.nv_s[1]};
+    float* const scale[2] = {a.ks + at, a.vs + at};
+    uint8_t* const dst[2] = {a.k + at * P * D, a.v + at * P * D};
+
+    u32x4 x[2][KEEP][4];
+    auto load_unit = [&](int kv, int u, u32x4* y) SDPA_INLINE {
+        const int unit = lane + 64 * u, t = t_first + 4 * (unit / CH), c = unit % CH;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            y[k] = u32x4{};
+            if (t + k >= off && t + k < end) y[k] = *reinterpret_cast<const u32x4*>(src[kv] + (t + k) * row[kv] + 8 * c);
+        }
+    };
+    float amax[2] = {0.0f, 0.0f};
+    // whether token k of any lane's unit u is new: single tokens skip the rest
+    auto any_new = [&](int u, int k) SDPA_INLINE {
+        const int t = t_first + 4 * ((lane + 64 * u) / CH) + k;
+        return __builtin_amdgcn_ballot_w64(t >= off && t < end) != 0;
+    };
+    auto take_max = [&](int kv, int u, const u32x4* y) SDPA_INLINE {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (!any_new(u, k)) continue;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float f = Tr<T>::to_f((y[k][e >> 1] >> (16 * (e & 1))) & 0xffffu);
+                amax[kv] = fmaxf(amax[kv], finite(f) ? fabsf(f) : 0.0f);
+            }
+        }
+    };
+#pragma unroll
+    for (int u = KEEP; u < NU; ++u) {
+        if (64 * u >= units) break;
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) load_unit(kv, u, x[kv][u % KEEP]);
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) take_max(kv, u, x[kv][u % KEEP]);
+    }
+#pragma unroll
+    for (int u = 0; u < KEEP; ++u)
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) load_unit(kv, u, x[kv][u]);
+    float was[2], inv[2];
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv) was[kv] = off > 0 ? *scale[kv] : 0.0f;
+#pragma unroll
+    for (int u = 0; u < KEEP; ++u) {
+        if (64 * u >= units) break;
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) take_max(kv, u, x[kv][u]);
+    }
+#pragma unroll
+    for (int k = 1; k < 64; k *= 2)
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) amax[kv] = fmaxf(amax[kv], __shfl_xor(amax[kv], k));
+#pragma unroll
+    for (int kv = 0; kv < 2; ++kv) {
+        const float now = fmaxf(scale_for(amax[kv]), was[kv]);
+        inv[kv] = inverse(now);
+        if (lane == 0) *scale[kv] = now;
+        if (off > 0 && now > was[kv]) {  // the held codes move to the larger scale
+            if (kv == 0) rescale_held<D, P, false>(dst[0], off, was[0] * inv[0], lane);
+            else rescale_held<D, P, true>(dst[1], off, was[1] * inv[1], lane);
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < NU; ++u) {
+        if (64 * u >= units) break;
+        const int unit = lane + 64 * u, t = t_first + 4 * (unit / CH), c = unit % CH;
+#pragma unroll
+        for (int kv = 0; kv < 2; ++kv) {
+            if (u >= KEEP) load_unit(kv, u, x[kv][u % KEEP]);
+            if (t >= end) continue;
+            uint32_t code[4][2];  // [token][4 columns]
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                code[k][0] = code[k][1] = 0u;
+                if (!any_new(u, k)) continue;
+                float f[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) f[e] = Tr<T>::to_f((x[kv][u % KEEP][k][e >> 1] >> (16 * (e & 1))) & 0xffffu) * inv[kv];
+#pragma unroll
+                for (int e = 0; e < 2; ++e)
+                    code[k][e] = encode2(f[4 * e], f[4 * e + 1]) | encode2(f[4 * e + 2], f[4 * e + 3]) << 16;
+            }
+            if (kv == 0) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    if (t + k >= off && t + k < end) *reinterpret_cast<u32x2*>(dst[0] + (t + k) * D + 8 * c) = u32x2{code[k][0], code[k][1]};
+                continue;
+            }
+            const bool whole = t >= off && t + 4 <= end;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                uint32_t w = 0;
+#pragma unroll
+                for (int k = 0; k < 4; ++k) w |= ((code[k][e >> 2] >> (8 * (e & 3))) & 0xffu) << (8 * k);
+                uint8_t* p = dst[1] + (8 * c + e) * P + t;
+                if (whole) {
+                    *reinterpret_cast<uint32_t*>(p) = w;
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        if (t + k >= off && t + k < end) p[k] = (uint8_t)(w >> (8 * k));
+                }
+            }
+        }
+    }
+}
+
+template <typename T, int D>
+static int launch_append(const CacheArgs& a, hipStream_t s) {
+    const int64_t waves = (int64_t)a.B * a.Hkv * a.slots;
+    const dim3 grid((uint32_t)((waves + 3) / 4)), block(256);
+    switch (a.page) {
+        case 16: sdpa_cache_append_kernel<T, D, 16><<<grid, block, 0, s>>>(a); break;
+        case 32: sdpa_cache_append_kernel<T, D, 32><<<grid, block, 0, s>>>(a); break;
+        case 64: sdpa_cache_append_kernel<T, D, 64><<<grid, block, 0, s>>>(a); break;
+        default: sdpa_cache_append_kernel<T, D, 128><<<grid, block, 0, s>>>(a); break;
+    }
+    return (int)hipGetLastError();
+}
+
+template <typename T>
+static int launch_append_t(const CacheArgs& a, hipStream_t s) {
+    return a.D == 32 ? launch_append<T, 32>(a, s) : a.D == 64 ? launch_append<T, 64>(a, s) : launch_append<T, 128>(a, s);
+}
+
 int launch_cache_append(int dtype, const CacheArgs& a, void* stream) {
     hipStream_t s = static_cast<hipStream_t>(stream);
-    const dim3 grid(2u * a.B * a.Hkv * a.slots), block(256);
-    if (dtype == DT_F16) sdpa_cache_append_kernel<_Float16><<<grid, block, 0, s>>>(a);
-    else sdpa_cache_append_kernel<__bf16><<<grid, block, 0, s>>>(a);
-    return (int)hipGetLastError();
+    return dtype == DT_F16 ? launch_append_t<_Float16>(a, s) : launch_append_t<__bf16>(a, s);
 }
 
 // -------------------------------------------------------------------- attention
@@ -291,17 +375,17 @@ void sdpa_cache_attention_kernel(const CacheArgs a) {
     const int* const trow = a.table + b * a.table_s;
     const int first_cut = a.causal ? s.len - s.n + 1 : s.len;  // every row keeps the keys before it
 
-    for (int t0 = j0 + 64 * wave; t0 < j1; t0 += 64 * NW) {
-        // pages of this lane's key rows (16 (n / 4) ..) and of its values (16 g ..)
-        const int jk = t0 + 16 * (n >> 2), jv = t0 + 16 * g;
-        const int pk_raw = jk < s.len ? trow[jk >> a.page_log2] : -1;
-        const int pv_raw = jv < s.len ? trow[jv >> a.page_log2] : -1;
-        const bool okk = pk_raw >= 0 && pk_raw < a.n_pages, okv = pv_raw >= 0 && pv_raw < a.n_pages;
-        const int64_t pk = okk ? pk_raw : 0, pv = okv ? pv_raw : 0;
-        const int live = okv ? min(s.len - jv, 16) : 0;  // tokens of this lane that exist
-        const uint8_t* kp = a.k + ((pk * a.Hkv + h) * a.page + (jk & (a.page - 1)) + (n & 3)) * D + g * KB;
-        const uint8_t* vp = a.v + ((pv * a.Hkv + h) * D + n) * a.page + (jv & (a.page - 1));
-        uint32_t kc[4][KB / 4];
+    uint32_t odd = 0;
+    // The page of 16 tokens from j on (-1: none), of this lane's key rows
+    // (tokens 16 (n / 4) .. of a tile) and of its values (16 g ..). A tile's
+    // loads are spread over the loop: its pages a tile ahead, its keys behind
+    // the products of the tile before, its values ahead of its own products.
+    auto page_of = [&](int j) SDPA_INLINE -> int { return j < s.len ? trow[j >> a.page_log2] : -1; };
+    uint32_t kc[4][KB / 4];
+    auto load_keys = [&](int t0, int page) SDPA_INLINE {
+        const int64_t p = page >= 0 && page < a.n_pages ? page : 0;
+        const int j = t0 + 16 * (n >> 2);
+        const uint8_t* kp = a.k + ((p * a.Hkv + h) * a.page + (j & (a.page - 1)) + (n & 3)) * D + g * KB;
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
             if constexpr (KB >= 16) {
@@ -317,22 +401,32 @@ void sdpa_cache_attention_kernel(const CacheArgs a) {
                 kc[c][1] = x[1];
             }
         }
+    };
+    int t0 = j0 + 64 * wave;
+    int pk = -1, pv_raw = -1;
+    if (t0 < j1) {
+        pk = page_of(t0 + 16 * (n >> 2));
+        pv_raw = page_of(t0 + 16 * g);
+        load_keys(t0, pk);
+    }
+    for (; t0 < j1; t0 += 64 * NW) {
+        const int jv = t0 + 16 * g;
+        const bool okv = pv_raw >= 0 && pv_raw < a.n_pages;
+        const int64_t pv = okv ? pv_raw : 0;
+        const int live = okv ? min(s.len - jv, 16) : 0;  // tokens of this lane that exist
+        const uint8_t* vp = a.v + ((pv * a.Hkv + h) * D + n) * a.page + (jv & (a.page - 1));
         u32x4 vc[ND];
 #pragma unroll
         for (int d = 0; d < ND; ++d) vc[d] = *reinterpret_cast<const u32x4*>(vp + (int64_t)16 * d * a.page);
         const float ks = a.ks[pv * a.Hkv + h] * a.scale_log2, vs = a.vs[pv * a.Hkv + h];
+        const int next = t0 + 64 * NW;
+        if (next < j1) {
+            pk = page_of(next + 16 * (n >> 2));
+            pv_raw = page_of(next + 16 * g);
+        }
 
         const bool ragged = __builtin_amdgcn_ballot_w64(live < 16) != 0;
         const bool cut = ragged || t0 + 64 > first_cut;
-        if (ragged) {  // codes past the end may be anything, NaN among them
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int k = min(max(live - 4 * i, 0), 4);
-                const uint32_t mask = k == 4 ? 0xffffffffu : (1u << (8 * k)) - 1u;
-#pragma unroll
-                for (int d = 0; d < ND; ++d) vc[d][i] &= mask;
-            }
-        }
         f32x4 acc[RT][4];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
@@ -345,6 +439,7 @@ void sdpa_cache_attention_kernel(const CacheArgs a) {
                 for (int rt = 0; rt < RT; ++rt) acc[rt][c] = O::mfma(ka, qf[rt][e], acc[rt][c]);
             }
         }
+        if (next < j1) load_keys(next, pk);
         float top[RT];
         bool grow = false;
 #pragma unroll
@@ -382,46 +477,6 @@ void sdpa_cache_attention_kernel(const CacheArgs a) {
                     for (int r = 0; r < 4; ++r) oacc[rt][d][r] *= f;
             }
         }
-        if (cut) {
-            // NaN among the values, where a row may not keep it (0 times NaN
-            // would take it in): read as 0, and given to the rows that do
-            uint32_t odd = 0;
-#pragma unroll
-            for (int d = 0; d < ND; ++d)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) odd |= (vc[d][i] & 0x7f7f7f7fu) + 0x01010101u;
-            if (__builtin_amdgcn_ballot_w64((odd & 0x80808080u) != 0) != 0) {
-#pragma unroll
-                for (int rt = 0; rt < RT; ++rt) {
-                    bf16x8 kept[2];
-#pragma unroll
-                    for (int i = 0; i < 16; ++i)
-                        kept[i >> 3][i & 7] = (__bf16)(acc[rt][i >> 2][i & 3] == -INFINITY ? 0.0f : 1.0f);
-#pragma unroll
-                    for (int d = 0; d < ND; ++d) {
-                        f32x4 count = {};
-#pragma unroll
-                        for (int c = 0; c < 2; ++c) {
-                            uint32_t w[2];
-#pragma unroll
-                            for (int i = 0; i < 2; ++i) {
-                                const uint32_t x = vc[d][2 * c + i];
-                                w[i] = ((((x & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7) * 0x38u;  // 1.0 for NaN
-                            }
-                            count = OB::mfma(OB::widen(w[0], w[1]), kept[c], count);
-                        }
-#pragma unroll
-                        for (int r = 0; r < 4; ++r)
-                            if (count[r] != 0.0f) oacc[rt][d][r] = NAN;
-                    }
-                }
-#pragma unroll
-                for (int d = 0; d < ND; ++d)
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        vc[d][i] &= ~(((((vc[d][i] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7) * 0xffu);
-            }
-        }
         bf16x8 ph[RT][2], pl[RT][2];
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
@@ -439,6 +494,27 @@ void sdpa_cache_attention_kernel(const CacheArgs a) {
                 pl[rt][c] = Tr<__bf16>::lo8(p + 8 * c, ph[rt][c]);
             }
         }
+        if (ragged) {  // codes past the end may be anything, NaN among them
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int k = min(max(live - 4 * i, 0), 4);
+                const uint32_t mask = k == 4 ? 0xffffffffu : (1u << (8 * k)) - 1u;
+#pragma unroll
+                for (int d = 0; d < ND; ++d) vc[d][i] &= mask;
+            }
+        }
+        if (cut) {
+            // NaN among the values, where a row may not keep it (0 times NaN
+            // would take it in): read as 0 here, added to its rows at the end
+#pragma unroll
+            for (int d = 0; d < ND; ++d)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t nan = (((vc[d][i] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u) >> 7;
+                    odd |= nan;
+                    vc[d][i] &= ~(nan * 0xffu);
+                }
+        }
 #pragma unroll
         for (int d = 0; d < ND; ++d)
 #pragma unroll
@@ -450,6 +526,27 @@ void sdpa_cache_attention_kernel(const CacheArgs a) {
                     oacc[rt][d] = OB::mfma(va, pl[rt][c], oacc[rt][d]);
                 }
             }
+    }
+
+    // NaN values of this wave's tiles that not every row keeps, one token at a time
+    if (__builtin_amdgcn_ballot_w64(odd != 0) != 0) {
+        for (int t = j0 + 64 * wave; t < j1; t += 64 * NW) {
+            if (t + 64 <= first_cut) continue;
+            for (int j = t; j < min(t + 64, s.len); ++j) {
+                const int page = trow[j >> a.page_log2];
+                if (page < 0 || page >= a.n_pages) continue;
+                const uint8_t* vp = a.v + (((int64_t)page * a.Hkv + h) * D + 4 * g) * a.page + (j & (a.page - 1));
+#pragma unroll
+                for (int d = 0; d < ND; ++d)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        const bool nan = (vp[(16 * d + r) * a.page] & 0x7f) == 0x7f;
+#pragma unroll
+                        for (int rt = 0; rt < RT; ++rt)
+                            if (nan && j <= limit[rt]) oacc[rt][d][r] = NAN;
+                    }
+            }
+        }
     }
 
     // the four waves' rows joined
@@ -501,11 +598,38 @@ void sdpa_cache_attention_kernel(const CacheArgs a) {
 
 // The ranges joined: O and LSE of every row, and the weights plus each key's
 // sum of probabilities over the rows. Workgroups below n_rows take one row
-// each, the rest 256 keys each of one (sequence, key head).
+// each, the rest 256 keys each of one (sequence, key head). Latency bounds it:
+// a row's statistics are read by all threads at once.
+// reference and sum of a row from its ranges' statistics, read by `n` lanes (a
+// power of two) of which this is `lane`
+__device__ __forceinline__ float2 join_stats(const float2* ml, int nr, int lane, int n) {
+    float top = -INFINITY, sum = 0.0f;
+    for (int i0 = lane; i0 < nr; i0 += 4 * n) {
+        float2 e[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) e[k] = i0 + k * n < nr ? ml[i0 + k * n] : make_float2(-INFINITY, 0.0f);
+        float up = top;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) up = fmaxf(up, e[k].x);
+        if (up == -INFINITY) continue;
+        sum *= fast_exp2(top - up);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) sum += e[k].y * fast_exp2(e[k].x - up);
+        top = up;
+    }
+    for (int k = 1; k < n; k *= 2) {
+        const float t2 = __shfl_xor(top, k), s2 = __shfl_xor(sum, k), up = fmaxf(top, t2);
+        if (up != -INFINITY) sum = sum * fast_exp2(top - up) + s2 * fast_exp2(t2 - up);
+        top = up;
+    }
+    return make_float2(top, sum);
+}
+
 template <typename T>
 __global__ __attribute__((amdgpu_flat_work_group_size(256, 256)))
 void sdpa_cache_join_kernel(const CacheArgs a, int n_rows) {
     __shared__ float part[256];
+    __shared__ float factor[CACHE_MAX_RANGES];
     const int tid = threadIdx.x;
     if ((int)blockIdx.x < n_rows) {
         int id = blockIdx.x;
@@ -516,26 +640,35 @@ void sdpa_cache_join_kernel(const CacheArgs a, int n_rows) {
         if (r >= s.n * a.group) return;
         const int nr = max(1, (s.len + a.range_keys - 1) / a.range_keys);
         const int64_t at = (((int64_t)b * a.Hkv + h) * a.rows + r) * a.n_ranges;
-        float top = -INFINITY;
-        for (int i = 0; i < nr; ++i) top = fmaxf(top, a.ws_ml[at + i].x);
         const int per = 256 / a.D, d = tid % a.D, k = tid / a.D;
-        float sum = 0.0f, x = 0.0f;
-        for (int i = 0; i < nr; ++i) {
-            const float2 e = a.ws_ml[at + i];
-            const float f = e.x == -INFINITY ? 0.0f : fast_exp2(e.x - top);
-            sum += f * e.y;
-            if (f != 0.0f && i % per == k) x += f * a.ws_o[(at + i) * a.D + d];
+        const float* const ws = a.ws_o + at * a.D + d;
+        const float2 st = join_stats(a.ws_ml + at, nr, tid & 63, 64);
+        for (int i = tid; i < nr; i += 256) {
+            const float t = a.ws_ml[at + i].x;
+            factor[i] = t == -INFINITY ? 0.0f : fast_exp2(t - st.x);
+        }
+        __syncthreads();
+        float x = 0.0f;
+        for (int i0 = k; i0 < nr; i0 += 8 * per) {
+            float y[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = i0 + e * per < nr ? ws[(int64_t)(i0 + e * per) * a.D] : 0.0f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float f = factor[min(i0 + e * per, nr - 1)];
+                if (f != 0.0f) x += f * y[e];
+            }
         }
         part[tid] = x;
         __syncthreads();
         if (k != 0) return;
         for (int i = 1; i < per; ++i) x += part[i * a.D + d];
         const int tok = r / a.group, head = h * a.group + r - tok * a.group;
-        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+        const float inv = st.y == 0.0f ? 0.0f : 1.0f / st.y;
         static_cast<T*>(a.o)[head * a.o_s[0] + (int64_t)(s.q0 + tok) * a.o_s[1] + d] = (T)(x * inv);
         if (d == 0)
             a.lse[head * a.l_s[0] + (int64_t)(s.q0 + tok) * a.l_s[1]] =
-                sum == 0.0f ? -INFINITY : (top + __builtin_amdgcn_logf(sum)) * LN2;
+                st.y == 0.0f ? -INFINITY : (st.x + __builtin_amdgcn_logf(st.y)) * LN2;
         return;
     }
     int id = blockIdx.x - n_rows;
@@ -548,25 +681,26 @@ void sdpa_cache_join_kernel(const CacheArgs a, int n_rows) {
     const int rows = s.n * a.group;
     const int64_t row0 = ((int64_t)b * a.Hkv + h) * a.rows;
     const float w = j < a.w_cols ? a.w_in[b * a.wi_s[0] + h * a.wi_s[1] + j] : 0.0f;
+    const bool live = j < min(s.len, a.w_cols);
     float x = 0.0f;  // the rows' sum first, so that adding it to the weight rounds once
-    for (int r0 = 0; r0 < rows; r0 += 256) {  // LSE of up to 256 rows at a time
+    for (int r0 = 0; r0 < rows && j - tid < s.len; r0 += 32) {  // LSE of 32 rows at a time, eight lanes each
+        const int r = r0 + (tid >> 3);
+        float2 st = make_float2(-INFINITY, 0.0f);
+        if (r < rows) st = join_stats(a.ws_ml + (row0 + r) * a.n_ranges, nr, tid & 7, 8);
         __syncthreads();
-        float lse2 = INFINITY;  // a row without keys adds nothing
-        if (r0 + tid < rows) {
-            const int64_t at = (row0 + r0 + tid) * a.n_ranges;
-            float top = -INFINITY, sum = 0.0f;
-            for (int i = 0; i < nr; ++i) top = fmaxf(top, a.ws_ml[at + i].x);
-            for (int i = 0; i < nr; ++i) {
-                const float2 e = a.ws_ml[at + i];
-                sum += e.x == -INFINITY ? 0.0f : e.y * fast_exp2(e.x - top);
+        if ((tid & 7) == 0) part[tid >> 3] = st.y == 0.0f ? INFINITY : st.x + __builtin_amdgcn_logf(st.y);
+        __syncthreads();
+        if (live) {
+            const float* const tp = a.ws_t + (row0 + r0) * a.t_cols + j;
+            const int n = min(32, rows - r0);
+            for (int i0 = 0; i0 < n; i0 += 4) {
+                float t[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) t[e] = i0 + e < n ? tp[(int64_t)(i0 + e) * a.t_cols] : -INFINITY;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x += fast_exp2(t[e] - part[min(i0 + e, n - 1)]);
             }
-            if (sum != 0.0f) lse2 = top + __builtin_amdgcn_logf(sum);
         }
-        part[tid] = lse2;
-        __syncthreads();
-        if (j < s.len)
-            for (int r = r0; r < min(rows, r0 + 256); ++r)
-                x += fast_exp2(a.ws_t[(row0 + r) * a.t_cols + j] - part[r - r0]);
     }
     if (j < a.w_cols) a.w_out[b * a.wo_s[0] + h * a.wo_s[1] + j] = w + x;
 }

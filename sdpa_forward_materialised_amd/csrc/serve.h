@@ -98,6 +98,7 @@ struct CacheArgs {
 int launch_cache_append(int dtype, const CacheArgs& a, void* stream);
 int launch_cache_attention(int dtype, const CacheArgs& a, void* stream);
 int launch_cache_evict(const CacheArgs& a, void* stream);
+constexpr int CACHE_MAX_RANGES = 512;  // key ranges of a call, at most
 // query rows of one workgroup of the attention kernel, given the rows of a call
 inline int cache_block_rows(int rows) { return rows <= 16 ? 16 : 32; }
 
