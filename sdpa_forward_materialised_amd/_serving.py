@@ -17,9 +17,46 @@ from typing import Optional, Tuple
 
 import torch
 
-from ._binding import _causal_code, _check_devices, _current_stream, _desc, _raise, load_library
+from ._binding import _DTYPES, _PACK, _causal_code, _current_stream, _raise, load_library
 
 _BYTES = {}  # workspace bytes per call signature (shapes and flags)
+_PACK2, _PACK3, _PACK4 = (_PACK[n].pack for n in (2, 3, 4))
+
+# These calls often take a few microseconds on the GPU, so the host path is
+# kept short: tensors are described in one go, without the dense binding's
+# right-alignment, and devices compared as indices.
+
+
+def _dtype(t: torch.Tensor) -> int:
+    dt = _DTYPES.get(t.dtype)
+    if dt is None:
+        raise ValueError(f"unsupported dtype {t.dtype}")
+    return dt
+
+
+def _desc2(name: str, t: torch.Tensor) -> bytes:
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have 2 dims, got {t.dim()}")
+    return _PACK2(t.data_ptr(), _dtype(t), 2, *t.shape, *t.stride())
+
+
+def _desc3(name: str, t: torch.Tensor) -> bytes:
+    if t.dim() != 3:
+        raise ValueError(f"{name} must have 3 dims, got {t.dim()}")
+    return _PACK3(t.data_ptr(), _dtype(t), 3, *t.shape, *t.stride())
+
+
+def _device(t: torch.Tensor, *others: torch.Tensor) -> int:
+    """Index of the GPU that all of the tensors are on."""
+    i = t.get_device()
+    if i < 0:
+        raise ValueError("sdpa_math runs on the GPU only: every tensor must be a cuda tensor")
+    for o in others:
+        if o.get_device() != i:
+            if not o.is_cuda:
+                raise ValueError("sdpa_math runs on the GPU only: every tensor must be a cuda tensor")
+            raise ValueError(f"tensors on different devices ({t.device} and {o.device})")
+    return i
 
 
 class PagedCache:
@@ -31,7 +68,7 @@ class PagedCache:
     multiplied with. The tensors must keep their storage while the object lives.
     """
 
-    __slots__ = ("k", "v", "k_scale", "v_scale", "_bytes", "_device")
+    __slots__ = ("k", "v", "k_scale", "v_scale", "_bytes")
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor):
         for name, t, nd in (("k", k, 4), ("v", v, 4), ("k_scale", k_scale, 2), ("v_scale", v_scale, 2)):
@@ -40,8 +77,9 @@ class PagedCache:
             if t.device != k.device:
                 raise ValueError(f"cache tensors on different devices ({k.device} and {t.device})")
         self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
-        self._bytes = _desc(k, 4) + _desc(v, 4) + _desc(k_scale, 2) + _desc(v_scale, 2)
-        self._device = k.device
+        self._bytes = b"".join((_PACK4(k.data_ptr(), _dtype(k), 4, *k.shape, *k.stride()),
+                                _PACK4(v.data_ptr(), _dtype(v), 4, *v.shape, *v.stride()),
+                                _desc2("k_scale", k_scale), _desc2("v_scale", v_scale)))
 
     @property
     def page_tokens(self) -> int:
@@ -54,6 +92,13 @@ def new_cache(n_pages: int, heads: int, head_dim: int, page_tokens: int = 64, de
                       torch.zeros((n_pages, heads, head_dim, page_tokens), dtype=torch.float8_e4m3fn, device=device),
                       torch.zeros((n_pages, heads), dtype=torch.float32, device=device),
                       torch.zeros((n_pages, heads), dtype=torch.float32, device=device))
+
+
+# torch's current device and stream (its own raw queries when it has them:
+# the tensors of a call are on the GPU already, so nothing is left to initialise)
+_current_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda i: _current_stream(torch.device("cuda", i)))
 
 
 def _offsets(name: str, t: torch.Tensor, n: Optional[int] = None) -> None:
@@ -70,11 +115,6 @@ def _table(name: str, t: torch.Tensor, n_seqs: int) -> None:
         raise ValueError(f"{name} has {t.shape[0]} rows, expected {n_seqs}")
 
 
-def _packed(name: str, t: torch.Tensor) -> None:
-    if t.dim() != 3:
-        raise ValueError(f"{name} must be 3-D [T, H, D]")
-
-
 def _cu_pair(cu_q: torch.Tensor, cu_kv: torch.Tensor) -> int:
     _offsets("cu_seqlens_q", cu_q)
     _offsets("cu_seqlens_kv", cu_kv)
@@ -89,18 +129,18 @@ def _scale(scale: Optional[float], D: int) -> float:
     return 1.0 / math.sqrt(D) if D > 0 else 1.0
 
 
-def _call(lib, fn, dev: torch.device, *args) -> None:
+def _call(lib, fn, dev: int, *args) -> None:
     """``fn(*args, stream)`` on the tensors' device (made current only when it is not)."""
-    if dev.index == torch.cuda.current_device():
-        rc = fn(*args, _current_stream(dev))
+    if dev == _current_device():
+        rc = fn(*args, _raw_stream(dev))
     else:
         with torch.cuda.device(dev):
-            rc = fn(*args, _current_stream(dev))
+            rc = fn(*args, _raw_stream(dev))
     if rc != 0:
         _raise(rc, lib)
 
 
-def _workspace(lib, fn, dev: torch.device, sig, *args):
+def _workspace(lib, fn, like: torch.Tensor, sig, *args):
     """(workspace or None, its bytes) of a call with this signature."""
     n = _BYTES.get(sig)
     if n is None:
@@ -111,7 +151,16 @@ def _workspace(lib, fn, dev: torch.device, sig, *args):
         if len(_BYTES) >= 4096:  # many distinct shapes: start over rather than grow
             _BYTES.clear()
         n = _BYTES[sig] = c.value
-    return (torch.empty(n, dtype=torch.uint8, device=dev), n) if n > 0 else (None, 0)
+    return (like.new_empty(n, dtype=torch.uint8), n) if n > 0 else (None, 0)
+
+
+def _outputs(q: torch.Tensor, out) -> Tuple[torch.Tensor, torch.Tensor]:
+    if out is None:
+        T, H, D = q.shape
+        return q.new_empty((T, H, D)), q.new_empty((T, H), dtype=torch.float32)
+    O, L = out
+    _device(q, O, L)
+    return O, L
 
 
 def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens_q: torch.Tensor,
@@ -123,19 +172,14 @@ def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqle
     Arguments as ``fwd_varlen``, except that it is causal by default; ``out``
     may pass (O, LSE). Tokens of no sequence are not written."""
     lib = load_library()
-    dev = _check_devices(q, k, v, cu_seqlens_q, cu_seqlens_kv)
+    dev = _device(q, k, v, cu_seqlens_q, cu_seqlens_kv)
     n = _cu_pair(cu_seqlens_q, cu_seqlens_kv)
     causal = _causal_code(is_causal, causal_alignment)
-    _packed("q", q), _packed("k", k), _packed("v", v)
-    if out is None:
-        O = torch.empty(q.shape, dtype=q.dtype, device=dev)
-        L = torch.empty(q.shape[:2], dtype=torch.float32, device=dev)
-    else:
-        O, L = out
-        _check_devices(q, O, L)
-    _call(lib, lib.sdpa_prompt_fwd, dev, _desc(q, 3), _desc(k, 3), _desc(v, 3), cu_seqlens_q.data_ptr(),
-          cu_seqlens_kv.data_ptr(), n, int(max_seqlen_q), int(max_seqlen_kv), causal, _scale(scale, q.shape[2]),
-          int(bool(enable_gqa)), _desc(O, 3), _desc(L, 2))
+    dq, dk, dv = _desc3("q", q), _desc3("k", k), _desc3("v", v)
+    O, L = _outputs(q, out)
+    _call(lib, lib.sdpa_prompt_fwd, dev, dq, dk, dv, cu_seqlens_q.data_ptr(), cu_seqlens_kv.data_ptr(), n,
+          int(max_seqlen_q), int(max_seqlen_kv), causal, _scale(scale, q.shape[2]), int(bool(enable_gqa)),
+          _desc3("out", O), _desc2("lse", L))
     return O, L
 
 
@@ -150,21 +194,20 @@ def key_weights(q: torch.Tensor, k: torch.Tensor, lse: torch.Tensor, cu_seqlens_
     ``out`` may pass the result's tensor (last dim contiguous: a slice of the
     weights that ``cache_attention`` adds to, for instance)."""
     lib = load_library()
-    dev = _check_devices(q, k, lse, cu_seqlens_q, cu_seqlens_kv)
+    dev = _device(q, k, lse, cu_seqlens_q, cu_seqlens_kv)
     n = _cu_pair(cu_seqlens_q, cu_seqlens_kv)
     causal = _causal_code(is_causal, causal_alignment)
-    _packed("q", q), _packed("k", k)
+    dq, dk = _desc3("q", q), _desc3("k", k)
     max_q, max_kv, gqa = int(max_seqlen_q), int(max_seqlen_kv), int(bool(enable_gqa))
     if out is None:
-        out = torch.empty((n, k.shape[1], max(0, max_kv)), dtype=torch.float32, device=dev)
+        out = q.new_empty((n, k.shape[1], max(0, max_kv)), dtype=torch.float32)
     else:
-        _check_devices(q, out)
-    dq, dk = _desc(q, 3), _desc(k, 3)
-    ws, nbytes = _workspace(lib, lib.sdpa_key_weights_workspace_bytes, dev,
+        _device(q, out)
+    ws, nbytes = _workspace(lib, lib.sdpa_key_weights_workspace_bytes, q,
                             ("weights", q.shape, k.shape, q.dtype, n, max_q, max_kv), dq, dk, n, max_q, max_kv, 1)
-    _call(lib, lib.sdpa_key_weights, dev, dq, dk, _desc(lse, 2), cu_seqlens_q.data_ptr(), cu_seqlens_kv.data_ptr(), n,
-          max_q, max_kv, causal, _scale(scale, q.shape[2]), gqa, _desc(out, 3), None if ws is None else ws.data_ptr(),
-          nbytes)
+    _call(lib, lib.sdpa_key_weights, dev, dq, dk, _desc2("lse", lse), cu_seqlens_q.data_ptr(), cu_seqlens_kv.data_ptr(), n,
+          max_q, max_kv, causal, _scale(scale, q.shape[2]), gqa, _desc3("out", out),
+          None if ws is None else ws.data_ptr(), nbytes)
     return out
 
 
@@ -175,13 +218,12 @@ def cache_append(cache: PagedCache, k: torch.Tensor, v: torch.Tensor, page_table
     ``kv_lens`` [n_seqs] tokens that the sequences hold. ``page_table``
     [n_seqs, max_pages] lists their pages. ``kv_lens`` is not changed."""
     lib = load_library()
-    dev = _check_devices(cache.k, k, v, page_table, kv_lens, cu_seqlens)
+    dev = _device(cache.k, k, v, page_table, kv_lens, cu_seqlens)
     n = kv_lens.shape[0] if kv_lens.dim() == 1 else -1
     _offsets("kv_lens", kv_lens)
     _offsets("cu_seqlens", cu_seqlens, n + 1)
     _table("page_table", page_table, n)
-    _packed("k", k), _packed("v", v)
-    _call(lib, lib.sdpa_cache_append, dev, cache._bytes, _desc(k, 3), _desc(v, 3), page_table.data_ptr(), n,
+    _call(lib, lib.sdpa_cache_append, dev, cache._bytes, _desc3("k", k), _desc3("v", v), page_table.data_ptr(), n,
           page_table.shape[1], page_table.stride(0), kv_lens.data_ptr(), cu_seqlens.data_ptr(), int(max_new))
 
 
@@ -198,32 +240,29 @@ def cache_attention(q: torch.Tensor, cache: PagedCache, page_table: torch.Tensor
     head's query heads and the new tokens, is added to them, in place or into
     ``weights_out``."""
     lib = load_library()
-    dev = _check_devices(q, cache.k, page_table, kv_lens, cu_seqlens_q, weights, weights_out)
+    dev = _device(q, cache.k, page_table, kv_lens, cu_seqlens_q)
     n = kv_lens.shape[0] if kv_lens.dim() == 1 else -1
     _offsets("kv_lens", kv_lens)
     _offsets("cu_seqlens_q", cu_seqlens_q, n + 1)
     _table("page_table", page_table, n)
-    _packed("q", q)
-    if weights is None and weights_out is not None:
+    dq, gqa = _desc3("q", q), int(bool(enable_gqa))
+    dw = dwo = None
+    if weights is not None:
+        if weights_out is None:
+            weights_out = weights
+        _device(q, weights, weights_out)
+        dw, dwo = _desc3("weights", weights), _desc3("weights_out", weights_out)
+    elif weights_out is not None:
         raise ValueError("weights_out needs weights")
-    if weights is not None and weights_out is None:
-        weights_out = weights
     max_pages, max_q, gather = page_table.shape[1], int(max_seqlen_q), int(weights is not None)
     max_kv = max_pages * cache.k.shape[2] if max_kv is None else int(max_kv)
-    if out is None:
-        O = torch.empty(q.shape, dtype=q.dtype, device=dev)
-        L = torch.empty(q.shape[:2], dtype=torch.float32, device=dev)
-    else:
-        O, L = out
-        _check_devices(q, O, L)
-    dq, gqa = _desc(q, 3), int(bool(enable_gqa))
-    ws, nbytes = _workspace(lib, lib.sdpa_cache_attention_workspace_bytes, dev,
+    O, L = _outputs(q, out)
+    ws, nbytes = _workspace(lib, lib.sdpa_cache_attention_workspace_bytes, q,
                             ("cache", q.shape, cache.k.shape, n, max_pages, max_q, max_kv, gqa, gather), dq,
                             cache._bytes, n, max_pages, max_q, max_kv, gqa, gather)
     _call(lib, lib.sdpa_cache_attention, dev, dq, cache._bytes, page_table.data_ptr(), n, max_pages,
           page_table.stride(0), kv_lens.data_ptr(), cu_seqlens_q.data_ptr(), max_q, max_kv, int(bool(is_causal)),
-          _scale(scale, q.shape[2]), gqa, None if weights is None else _desc(weights, 3),
-          None if weights is None else _desc(weights_out, 3), _desc(O, 3), _desc(L, 2),
+          _scale(scale, q.shape[2]), gqa, dw, dwo, _desc3("out", O), _desc2("lse", L),
           None if ws is None else ws.data_ptr(), nbytes)
     return O, L
 
@@ -239,7 +278,9 @@ def cache_evict(cache: PagedCache, page_table: torch.Tensor, kv_lens: torch.Tens
     ``weights_out``. Returns (the positions kept, int32 [n_seqs, Hkv, budget]
     with -1 behind them; the new lengths, int32 [n_seqs])."""
     lib = load_library()
-    dev = _check_devices(cache.k, page_table, kv_lens, weights, weights_out, to_table)
+    if weights_out is None:
+        weights_out = weights
+    dev = _device(cache.k, page_table, kv_lens, weights, weights_out, to_table)
     n = kv_lens.shape[0] if kv_lens.dim() == 1 else -1
     _offsets("kv_lens", kv_lens)
     _table("page_table", page_table, n)
@@ -247,11 +288,9 @@ def cache_evict(cache: PagedCache, page_table: torch.Tensor, kv_lens: torch.Tens
     budget = int(budget)
     if budget < 1:
         raise ValueError("budget must be at least 1")
-    if weights_out is None:
-        weights_out = weights
-    kept = torch.empty((n, cache.k.shape[1], budget), dtype=torch.int32, device=dev)
-    lens = torch.empty((n,), dtype=torch.int32, device=dev)
+    kept = kv_lens.new_empty((n, cache.k.shape[1], budget))
+    lens = kv_lens.new_empty((n,))
     _call(lib, lib.sdpa_cache_evict, dev, cache._bytes, page_table.data_ptr(), n, page_table.shape[1],
-          page_table.stride(0), kv_lens.data_ptr(), _desc(weights, 3), _desc(weights_out, 3), budget, int(recent),
+          page_table.stride(0), kv_lens.data_ptr(), _desc3("weights", weights), _desc3("weights_out", weights_out), budget, int(recent),
           to_table.data_ptr(), to_table.shape[1], to_table.stride(0), kept.data_ptr(), lens.data_ptr())
     return kept, lens
