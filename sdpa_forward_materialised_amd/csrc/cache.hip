@@ -734,14 +734,15 @@ int launch_cache_attention(int dtype, const CacheArgs& a, void* stream) {
 // sdpa_cache_select_kernel: one workgroup per (sequence, key head) finds the
 // tokens to keep. The weights of the candidates (the tokens before the recent
 // ones) become integers of the same order (NaN highest), kept in LDS where
-// they fit; a radix histogram of 11, 11 and 10 bits, the first one taken while
-// the weights are loaded, the last over a list of the tokens that share the
-// bits found so far, gives the value of the last candidate kept. One more pass
-// marks the kept ones and those tied with the last, as bits of a word for
-// every 64 tokens, and after a scan over the waves' counts each wave emits its
-// kept tokens in order, of the tied ones the first. Counts are integers and
-// the list's order has no effect, so the atomics leave nothing to chance. One
-// CU's latencies bound it.
+// they fit; a radix histogram of 11, 11 and 10 bits gives the value of the last
+// candidate kept. Its first part is taken while the weights are loaded; then
+// one pass marks what is above the bits found, as bits of a word for every 64
+// tokens, and lists what shares them (few, unless many weights are nearly
+// equal: then every pass goes over all), and the rest goes by the list. After a
+// scan over the waves' counts each wave emits its kept tokens in order, of
+// those tied with the last the first. Counts are integers and the list's order
+// has no effect, so the atomics leave nothing to chance. One CU's instructions
+// bound it: 32768 tokens 30 us, 4096 12 (MI355X).
 __device__ __forceinline__ uint32_t order_key(float x) {
     const uint32_t u = __builtin_bit_cast(uint32_t, x);
     const uint32_t k = u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);  // negative: all bits turn, else the sign
@@ -766,7 +767,7 @@ void sdpa_cache_select_kernel(const CacheArgs a) {
     __shared__ __attribute__((aligned(16))) uint32_t keys[CAP > 0 ? CAP : 1];
     __shared__ uint64_t kept_bits[WORDS], tied_bits[WORDS];
     __shared__ int hist[NB];
-    __shared__ uint32_t list[SELECT_LIST];
+    __shared__ uint2 list[SELECT_LIST];  // key, token
     __shared__ int wsum[NWV], wtie[NWV];
     __shared__ int pick_s, above_s, bin_s, list_n;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -814,16 +815,16 @@ void sdpa_cache_select_kernel(const CacheArgs a) {
     clear();
     if (tid == 0) list_n = 0;
     __syncthreads();
-    for (int i = 0; i < words; i += 8) {  // every key, and the histogram of the highest bits
-        float x[8];
-        const int m = min(8, words - i);
+    for (int i = 0; i < words; i += 16) {  // every key, and the histogram of the highest bits
+        float x[16];
+        const int m = min(16, words - i);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
+        for (int e = 0; e < 16; ++e) {
             const int j = t0 + 64 * (i + e);
             x[e] = e < m && j < late ? w[j] : 0.0f;
         }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
+        for (int e = 0; e < 16; ++e) {
             if (e >= m) break;
             const int j = t0 + 64 * (i + e);
             const uint32_t k = j < late ? order_key(x[e]) : 0u;
@@ -834,30 +835,45 @@ void sdpa_cache_select_kernel(const CacheArgs a) {
     // the largest `pick` that `take` candidates reach, and how many of those equal to it are kept
     uint32_t pick = 0;
     int need = take;
+    bool listed = false;
     if (some) {
         uint32_t mask = 0;
         for (int pass = 0; pass < 3; ++pass) {
             const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1024 : 2048;
-            const bool listed = pass == 2 && bin_s <= SELECT_LIST;  // bin_s: tokens that share the first 11 bits
             if (pass > 0) {
                 clear();
+                if (pass == 1) {
+                    listed = CAP > 0 && bin_s <= SELECT_LIST;  // bin_s: tokens that share the first 11 bits
+                    if (listed) {
+                        // mark what is above these bits, and list what shares them
+                        for (int i = 0; i < words; i += 4) {
+                            uint32_t k[4];
+                            four(i, k);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const bool in = (k[e] & mask) == pick;
+                                const uint64_t kb = __builtin_amdgcn_ballot_w64((k[e] & mask) > pick);
+                                if (lane == 0) {
+                                    kept_bits[wave * words + i + e] = kb;
+                                    tied_bits[wave * words + i + e] = 0;
+                                }
+                                if (in) list[atomicAdd(&list_n, 1)] = make_uint2(k[e], (uint32_t)(t0 + 64 * (i + e)));
+                            }
+                        }
+                    }
+                }
                 __syncthreads();
                 if (listed) {
                     for (int i = tid & ~63; i < list_n; i += NT) {
-                        const uint32_t k = i + lane < list_n ? list[i + lane] : 0u;
+                        const uint32_t k = i + lane < list_n ? list[i + lane].x : 0u;
                         add((int)(k >> shift) & (bins - 1), (k & mask) == pick);
                     }
                 } else {
-                    const bool make = pass == 1 && bin_s <= SELECT_LIST;
                     for (int i = 0; i < words; i += 4) {
                         uint32_t k[4];
                         four(i, k);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const bool in = (k[e] & mask) == pick;
-                            add((int)(k[e] >> shift) & (bins - 1), in);
-                            if (make && in) list[atomicAdd(&list_n, 1)] = k[e];
-                        }
+                        for (int e = 0; e < 4; ++e) add((int)(k[e] >> shift) & (bins - 1), (k[e] & mask) == pick);
                     }
                 }
             }
@@ -895,19 +911,38 @@ void sdpa_cache_select_kernel(const CacheArgs a) {
     }
     // mark and count
     int cnt = 0, tie = 0;
-    for (int i = 0; i < words; i += 4) {
-        uint32_t k[4];
-        four(i, k);
+    if (listed) {
+        for (int i = tid; i < list_n; i += NT) {
+            const uint2 e = list[i];
+            if (e.x < pick) continue;
+            unsigned long long* const bits = reinterpret_cast<unsigned long long*>(e.x > pick ? kept_bits : tied_bits);
+            atomicOr(&bits[e.y >> 6], 1ull << (e.y & 63));
+        }
+        __syncthreads();
+        for (int i = lane; i < words; i += 64) {
+            cnt += __popcll(kept_bits[wave * words + i]);
+            tie += __popcll(tied_bits[wave * words + i]);
+        }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const uint64_t kb = __builtin_amdgcn_ballot_w64(k[e] > pick);
-            const uint64_t tb = __builtin_amdgcn_ballot_w64(k[e] == pick && pick != 0);
-            cnt += __popcll(kb);
-            tie += __popcll(tb);
-            if constexpr (CAP > 0) {
-                if (lane == 0) {
-                    kept_bits[wave * words + i + e] = kb;
-                    tied_bits[wave * words + i + e] = tb;
+        for (int k = 1; k < 64; k *= 2) {
+            cnt += __shfl_xor(cnt, k);
+            tie += __shfl_xor(tie, k);
+        }
+    } else {
+        for (int i = 0; i < words; i += 4) {
+            uint32_t k[4];
+            four(i, k);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint64_t kb = __builtin_amdgcn_ballot_w64(k[e] > pick);
+                const uint64_t tb = __builtin_amdgcn_ballot_w64(k[e] == pick && pick != 0);
+                cnt += __popcll(kb);
+                tie += __popcll(tb);
+                if constexpr (CAP > 0) {
+                    if (lane == 0) {
+                        kept_bits[wave * words + i + e] = kb;
+                        tied_bits[wave * words + i + e] = tb;
+                    }
                 }
             }
         }
@@ -923,28 +958,34 @@ void sdpa_cache_select_kernel(const CacheArgs a) {
         ties += wtie[i];
     }
     const uint64_t below = (uint64_t(1) << lane) - 1;
-    for (int i = 0; i < words; ++i) {
-        uint64_t kb, tb;
-        uint32_t k = 0;
-        if constexpr (CAP > 0) {
-            kb = kept_bits[wave * words + i];
-            tb = tied_bits[wave * words + i];
-            k = keys[t0 + 64 * i];
-        } else {
-            const int j = t0 + 64 * i;
-            k = j < late ? order_key(w[j]) : 0u;
-            kb = __builtin_amdgcn_ballot_w64(k > pick);
-            tb = __builtin_amdgcn_ballot_w64(k == pick && pick != 0);
+    for (int i0 = 0; i0 < words; i0 += 4) {
+        uint64_t kb[4], tb[4];
+        uint32_t k[4];
+        four(i0, k);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if constexpr (CAP > 0) {
+                kb[e] = kept_bits[wave * words + i0 + e];
+                tb[e] = tied_bits[wave * words + i0 + e];
+            } else {
+                kb[e] = __builtin_amdgcn_ballot_w64(k[e] > pick);
+                tb[e] = __builtin_amdgcn_ballot_w64(k[e] == pick && pick != 0);
+            }
         }
-        const bool tied = (tb >> lane & 1) && ties + __popcll(tb & below) < need;
-        kb |= __builtin_amdgcn_ballot_w64(tied);
-        ties += __popcll(tb);
-        if (kb >> lane & 1) {
-            const int to = at + __popcll(kb & below);
-            kept[to] = t0 + 64 * i;
-            if constexpr (CAP > 0) wo[to] = key_value(k);  // in place too: every candidate is in LDS
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (tb[e] != 0) {
+                const bool tied = (tb[e] >> lane & 1) && ties + __popcll(tb[e] & below) < need;
+                kb[e] |= __builtin_amdgcn_ballot_w64(tied);
+                ties += __popcll(tb[e]);
+            }
+            if (kb[e] >> lane & 1) {
+                const int to = at + __popcll(kb[e] & below);
+                kept[to] = t0 + 64 * (i0 + e);
+                if constexpr (CAP > 0) wo[to] = key_value(k[e]);  // in place too: every candidate is in LDS
+            }
+            at += __popcll(kb[e]);
         }
-        at += __popcll(kb);
     }
     for (int i = tid; i < len - late; i += NT) kept[take + i] = late + i;
     for (int i = n + tid; i < a.budget; i += NT) kept[i] = -1;
