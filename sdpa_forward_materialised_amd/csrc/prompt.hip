@@ -1,14 +1,16 @@
 // Attention over packed prompts without the probability map, and the weight
 // that every key of those prompts received.
 //
-// sdpa_prompt_kernel: O = softmax(scale Q K^T) V and the row log-sum-exp, in
-// one sweep over the keys. With a running reference m_i >= max_j s_ij - 8 (in
-// base 2) of every row, l_i = sum_j 2^(s_ij - m_i) and
-// A_i = sum_j 2^(s_ij - m_i) v_j are updated tile by tile; a tile whose row
-// maximum passes m_i + 8 raises m_i and scales l_i and A_i by 2^(old - new).
-// O_i = A_i / l_i, LSE_i = (m_i + log2 l_i) ln 2. A reference up to 2^8 below
-// the maximum loses nothing (float32 sums, 16-bit floating weights keep their
-// relative precision) and most tiles then skip the scaling of A.
+// sdpa_prompt_kernel (16-bit types) and sdpa_prompt_f32_kernel:
+// O = softmax(scale Q K^T) V and the row log-sum-exp, in one sweep over the
+// keys. With a running reference m_i of every row, l_i = sum_j 2^(s_ij - m_i)
+// and A_i = sum_j 2^(s_ij - m_i) v_j are updated block by block (s in base 2);
+// a block whose weights pass a limit raises m_i to the row's maximum and scales
+// l_i and A_i by 2^(old - new). O_i = A_i / l_i, LSE_i = (m_i + log2 l_i) ln 2.
+// m_i is the maximum of some block, so l_i >= 1, and weights above 1, up to the
+// limit (2^8 in float32, 2^12 in the 16-bit types), lose nothing: the sums are
+// float32 and 16-bit floating weights keep their relative precision. Most
+// blocks then skip the scaling of A.
 #include "twopass.h"
 #include "serve.h"
 
@@ -173,41 +175,58 @@ __device__ __forceinline__ void add_kept(rsrc_t v, uint32_t row_bytes, int j0, i
             }
 }
 
+// O and LSE of the lane's row: x the sum of its half's columns relative to m, l its half of the weights
 template <typename T, int D>
-struct PromptCfg {
-    static constexpr int NW = 4;
-    static constexpr int RB = 1;                         // 32-row blocks per wave
-    static constexpr int TN = sizeof(T) == 2 ? 64 : 32;  // keys per tile
-    using C = TwoPassCfg<T, D, NW, MASK_NONE, true, TN, true>;
-    static constexpr int QB = 32 * RB * NW;
-    static constexpr int LDS_BYTES = 4 * C::TILEB;
-};
+__device__ __forceinline__ void store_rows(rsrc_t o, rsrc_t lse, const PackArgs& a, int row, bool ok, int hf, const f32x16* x, float m,
+                                           float l) {
+    const float sum = l + __shfl_xor(l, 32);
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    const uint32_t ooff = (uint32_t)((ok ? row : 0) * a.o_s[1] * (int)sizeof(T));
+#pragma unroll
+    for (int d = 0; d < D / 32; ++d) {
+        float y[16];
+#pragma unroll
+        for (int r = 0; r < 16; ++r) y[r] = x[d][r] * inv;
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+            if (a.o_vec) store8<T, true>(o, ooff, ok, 32 * d + 16 * c + 8 * hf, D, y + 8 * c);
+            else store8<T, false>(o, ooff, ok, 32 * d + 16 * c + 8 * hf, D, y + 8 * c);
+        }
+    }
+    const float z = sum == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(sum)) * LN2;
+    __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, z), lse,
+                                          pred(ok && hf == 0, (uint32_t)((ok ? row : 0) * a.l_s[1] * 4)), 0, 0);
+}
 
-template <typename T, int D>
-__global__ __attribute__((amdgpu_flat_work_group_size(256, 256), amdgpu_waves_per_eu(PromptCfg<T, D>::RB == 2 ? 1 : 2)))
-void sdpa_prompt_kernel(const PackArgs a) {
-    using P = PromptCfg<T, D>;
-    using C = typename P::C;
-    using TR = Tr<T>;
-    using vec = typename TR::vec;
-    constexpr int SZ = (int)sizeof(T), RB = P::RB, NW = P::NW, TN = P::TN, NKB = TN / 32, ND = D / 32;
+// float32: K and V tiles of 32 keys, double-buffered. The matrix instructions
+// (32x32x2, D / 2 of them for the scores and as many for the sums of a tile)
+// bound it. At D = 128 Q and the sums take 128 registers and the operands read
+// ahead the rest: one wave a SIMD, with up to 512 registers (16 heads of 4096
+// tokens, causal: 702 us, 98 TFLOP/s), where two waves of 256 spill (978 us).
+// Below that two waves fit and fill each other's waits (D = 64: 426 us).
+template <int D>
+__global__ __attribute__((amdgpu_flat_work_group_size(256, 256), amdgpu_waves_per_eu(D == 128 ? 1 : 2)))
+void sdpa_prompt_f32_kernel(const PackArgs a) {
+    constexpr int SZ = 4, NW = 4, TN = 32, QB = 32 * NW, ND = D / 32;
+    using C = TwoPassCfg<float, D, NW, MASK_NONE, true, TN, true>;
+    using TR = Tr<float>;
     constexpr int KSTEP = 2 * TR::KH, NKS = D / KSTEP;
-    __shared__ __attribute__((aligned(16))) uint8_t smem[P::LDS_BYTES];
+    __shared__ __attribute__((aligned(16))) uint8_t smem[4 * C::TILEB];
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 31, hf = lane >> 5;
     const PackWork w = pack_work(blockIdx.x, a.B, a.Hq, a.n_blk);
     const Seq s = sequence(a, w.b);
-    const int q0 = (a.n_blk - 1 - w.blk) * P::QB;
+    const int q0 = (a.n_blk - 1 - w.blk) * QB;
     if (q0 >= s.nq) return;
-    const int kend = a.causal ? min(s.nk, max(0, min(q0 + P::QB, s.nq) + s.coff)) : s.nk;
+    const int kend = a.causal ? min(s.nk, max(0, min(q0 + QB, s.nq) + s.coff)) : s.nk;
     const int ntiles = (kend + TN - 1) / TN;
     const int hk = w.h / a.group;
 
-    const rsrc_t qr = make_rsrc(static_cast<const T*>(a.q) + s.q0 * a.q_s[1] + w.h * a.q_s[0], a.q_ext);
-    const desc_t kd = make_desc(static_cast<const T*>(a.k) + s.k0 * a.k_s[1] + hk * a.k_s[0], a.k_ext);
-    const desc_t vd = make_desc(static_cast<const T*>(a.v) + s.k0 * a.v_s[1] + hk * a.v_s[0], a.v_ext);
-    const rsrc_t orr = make_rsrc(static_cast<T*>(a.o) + s.q0 * a.o_s[1] + w.h * a.o_s[0], a.o_ext);
+    const rsrc_t qr = make_rsrc(static_cast<const float*>(a.q) + s.q0 * a.q_s[1] + w.h * a.q_s[0], a.q_ext);
+    const desc_t kd = make_desc(static_cast<const float*>(a.k) + s.k0 * a.k_s[1] + hk * a.k_s[0], a.k_ext);
+    const desc_t vd = make_desc(static_cast<const float*>(a.v) + s.k0 * a.v_s[1] + hk * a.v_s[0], a.v_ext);
+    const rsrc_t orr = make_rsrc(static_cast<float*>(a.o) + s.q0 * a.o_s[1] + w.h * a.o_s[0], a.o_ext);
     const rsrc_t lr = make_rsrc(a.lse + s.q0 * a.l_s[1] + w.h * a.l_s[0], a.l_ext);
     const uint32_t krow = (uint32_t)(a.k_s[1] * SZ), vrow = (uint32_t)(a.v_s[1] * SZ);
 
@@ -226,126 +245,72 @@ void sdpa_prompt_kernel(const PackArgs a) {
     };
     static_assert(C::NI % NW == 0, "tile loads split evenly over the waves");
 
-    const int qw = q0 + wave * 32 * RB;  // this wave's first row
-    int qi[RB];
-    vec qf[RB][NKS];
+    const int qw = q0 + wave * 32, qi = qw + n;  // this wave's first row; this lane's
+    float qf[NKS];
+    const bool ok = qi < s.nq;
+    const uint32_t qoff = (uint32_t)((ok ? qi : 0) * a.q_s[1] * SZ);
+    uint32_t qo[NKS];
 #pragma unroll
-    for (int rb = 0; rb < RB; ++rb) {
-        qi[rb] = qw + 32 * rb + n;
-        const bool ok = qi[rb] < s.nq;
-        const uint32_t qoff = (uint32_t)((ok ? qi[rb] : 0) * a.q_s[1] * SZ);
-        uint32_t off[NKS];
-#pragma unroll
-        for (int c = 0; c < NKS; ++c) off[c] = pred(ok, qoff + (c * KSTEP + hf * TR::KH) * SZ);
-        load_operands<T, NKS>(qr, off, a.q_mul, qf[rb]);
-    }
-    f32x16 oacc[RB][ND];
-    float m[RB], l[RB];
+    for (int c = 0; c < NKS; ++c) qo[c] = pred(ok, qoff + (c * KSTEP + hf * TR::KH) * SZ);
+    load_operands<float, NKS>(qr, qo, a.q_mul, qf);
+    f32x16 oacc[ND];
+    float m, l;
     const int kr0 = swap23(n);
-    const int trg = lane >> 4, trs = lane & 15;
-    const int tr_row = 8 * (trg >> 1) + (trs >> 2);
-    const int tr_col = 16 * (trg & 1) + 4 * (((trs & 1) << 1) | ((trs >> 1) & 1));
 
-    auto tile = [&](int t, auto edge_c) SDPA_INLINE {
-        constexpr bool edge = decltype(edge_c)::value;
+    auto tile = [&](int t, bool edge) SDPA_INLINE {
         const uint8_t* const kt = smem + (t & 1) * 2 * C::TILEB;
         const uint8_t* const vt = kt + C::TILEB;
-        f32x16 acc[RB][NKB];
+        f32x16 acc = {};
 #pragma unroll
-        for (int kb = 0; kb < NKB; ++kb) {
-#pragma unroll
-            for (int rb = 0; rb < RB; ++rb) acc[rb][kb] = f32x16{};
-#pragma unroll
-            for (int c = 0; c < NKS; ++c) {
-                const int row = 32 * kb + kr0, elem = c * KSTEP + hf * TR::KH;
-                const uint8_t* p = kt + C::pos_k(row, elem * SZ / 16) * 16 + ((elem * SZ) & 15);
-                const vec ka = *reinterpret_cast<const vec*>(p);
-#pragma unroll
-                for (int rb = 0; rb < RB; ++rb) acc[rb][kb] = TR::mfma(ka, qf[rb][c], acc[rb][kb]);
-            }
+        for (int c = 0; c < NKS; ++c) {
+            const int elem = c * KSTEP + hf * TR::KH;
+            const float ka = *reinterpret_cast<const float*>(kt + C::pos_k(kr0, elem * SZ / 16) * 16 + ((elem * SZ) & 15));
+            acc = TR::mfma(ka, qf[c], acc);
         }
-        float top[RB];
-        bool grow = false;
+        if (edge) {
+            const int lim = min(s.nk - 1 - t * TN, a.causal ? qi + s.coff - t * TN : 0x7fffffff) - 8 * hf;
 #pragma unroll
-        for (int rb = 0; rb < RB; ++rb) {
-            if constexpr (edge) {
-#pragma unroll
-                for (int kb = 0; kb < NKB; ++kb) {
-                    const int jb = t * TN + 32 * kb;
-                    const int lim = min(s.nk - 1 - jb, a.causal ? qi[rb] + s.coff - jb : 0x7fffffff) - 8 * hf;
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) acc[rb][kb][r] = kk(0, r) > lim ? -INFINITY : acc[rb][kb][r];
-                }
-            }
-            float x = acc[rb][0][0];
-#pragma unroll
-            for (int i = 1; i < 16 * NKB; ++i) x = fmaxf(x, acc[rb][i >> 4][i & 15]);
-            top[rb] = x * a.scale_log2;
-            grow = grow || top[rb] > m[rb] + 8.0f;
+            for (int r = 0; r < 16; ++r) acc[r] = kk(0, r) > lim ? -INFINITY : acc[r];
         }
-        if (__builtin_amdgcn_ballot_w64(grow) != 0) {
+        float top = acc[0];
 #pragma unroll
-            for (int rb = 0; rb < RB; ++rb) {
-                const float up = fmaxf(m[rb], fmaxf(top[rb], __shfl_xor(top[rb], 32)));
-                const float f = up == -INFINITY ? 1.0f : fast_exp2(m[rb] - up);
-                m[rb] = up;
-                l[rb] *= f;
+        for (int r = 1; r < 16; ++r) top = fmaxf(top, acc[r]);
+        top *= a.scale_log2;
+        if (__builtin_amdgcn_ballot_w64(top > m + 8.0f) != 0) {
+            const float up = fmaxf(m, fmaxf(top, __shfl_xor(top, 32)));
+            const float f = up == -INFINITY ? 1.0f : fast_exp2(m - up);
+            m = up;
+            l *= f;
 #pragma unroll
-                for (int d = 0; d < ND; ++d)
+            for (int d = 0; d < ND; ++d)
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) oacc[rb][d][r] *= f;
-            }
+                for (int r = 0; r < 16; ++r) oacc[d][r] *= f;
         }
-        float p[RB][16 * NKB];
+        float p[16];
+        const float mu = m == -INFINITY ? 0.0f : m;
+        float sum = 0.0f;
 #pragma unroll
-        for (int rb = 0; rb < RB; ++rb) {
-            const float mu = m[rb] == -INFINITY ? 0.0f : m[rb];
-            float sum = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 16 * NKB; ++i) {
-                p[rb][i] = fast_exp2(__builtin_fmaf(acc[rb][i >> 4][i & 15], a.scale_log2, -mu));
-                sum += p[rb][i];
-            }
-            l[rb] += sum;
+        for (int r = 0; r < 16; ++r) {
+            p[r] = fast_exp2(__builtin_fmaf(acc[r], a.scale_log2, -mu));
+            sum += p[r];
         }
+        l += sum;
         // A^T += V^T P^T
-        if constexpr (SZ == 2) {
 #pragma unroll
-            for (int kc = 0; kc < 2 * NKB; ++kc) {  // 16 keys each
-                vec pv[RB];
+        for (int r = 0; r < 16; ++r) {
+            const int row = kk(hf, r);
 #pragma unroll
-                for (int rb = 0; rb < RB; ++rb) pv[rb] = TR::cvt8(p[rb] + 8 * kc);
-#pragma unroll
-                for (int d = 0; d < ND; ++d) {
-                    u32x2 half[2];
-#pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        const int row = 16 * kc + tr_row + 4 * r, col = 32 * d + tr_col;
-                        half[r] = lds_read_tr16(vt + C::pos_v(row, col * SZ / 16) * 16 + ((col * SZ) & 15));
-                    }
-                    const vec va = __builtin_bit_cast(vec, u32x4{half[0][0], half[0][1], half[1][0], half[1][1]});
-#pragma unroll
-                    for (int rb = 0; rb < RB; ++rb) oacc[rb][d] = TR::mfma(va, pv[rb], oacc[rb][d]);
-                }
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 16 * NKB; ++i) {
-                const int row = 32 * (i >> 4) + kk(hf, i & 15);
-#pragma unroll
-                for (int d = 0; d < ND; ++d) {
-                    const int col = 32 * d + swap23(n);
-                    const float va = *reinterpret_cast<const float*>(vt + C::pos_v(row, col * SZ / 16) * 16 + ((col * SZ) & 15));
-#pragma unroll
-                    for (int rb = 0; rb < RB; ++rb) oacc[rb][d] = TR::mfma(va, p[rb][i], oacc[rb][d]);
-                }
+            for (int d = 0; d < ND; ++d) {
+                const int col = 32 * d + swap23(n);
+                const float va = *reinterpret_cast<const float*>(vt + C::pos_v(row, col * SZ / 16) * 16 + ((col * SZ) & 15));
+                oacc[d] = TR::mfma(va, p[r], oacc[d]);
             }
         }
     };
 
     // tiles before t_full hold kept keys only, for every row of the wave;
     // tiles from t_end on none
-    const int last_row = min(qw + 32 * RB, s.nq) - 1;
+    const int last_row = min(qw + 32, s.nq) - 1;
     const bool live = qw < s.nq;
     const int t_end = !live ? 0 : a.causal ? max(0, min(ntiles, (last_row + s.coff + TN) / TN)) : ntiles;
     const int t_full = min(t_end, (a.causal ? max(0, min(s.nk, qw + s.coff + 1)) : s.nk) / TN);
@@ -353,62 +318,32 @@ void sdpa_prompt_kernel(const PackArgs a) {
     const int t_cut = (a.causal ? max(0, min(s.nk, q0 + s.coff + 1)) : s.nk) / TN;
     bool again = false;
     for (;;) {
+        m = -INFINITY;
+        l = 0.0f;
 #pragma unroll
-        for (int rb = 0; rb < RB; ++rb) {
-            m[rb] = -INFINITY;
-            l[rb] = 0.0f;
-#pragma unroll
-            for (int d = 0; d < ND; ++d) oacc[rb][d] = f32x16{};
-        }
+        for (int d = 0; d < ND; ++d) oacc[d] = f32x16{};
         if (ntiles > 0) load_tile(0);
         wait_copies<0>();
         __syncthreads();
         for (int t = 0; t < ntiles; ++t) {
             if (again && t >= t_cut) {
-                clean_tile<T, C::TILEB>(smem + ((t & 1) * 2 + 1) * C::TILEB, threadIdx.x);
+                clean_tile<float, C::TILEB>(smem + ((t & 1) * 2 + 1) * C::TILEB, threadIdx.x);
                 __syncthreads();
             }
             if (t + 1 < ntiles) load_tile(t + 1);
-            if (t < t_full) tile(t, std::false_type{});
-            else if (t < t_end) tile(t, std::true_type{});
+            if (t < t_end) tile(t, t >= t_full);
             wait_copies<0>();
             __syncthreads();
         }
         if (again || t_cut >= ntiles) break;
-        bool ok = true;
-#pragma unroll
-        for (int rb = 0; rb < RB; ++rb) ok = ok && all_finite<ND>(oacc[rb]);
-        again = __syncthreads_or(!ok) != 0;
+        again = __syncthreads_or(!all_finite<ND>(oacc)) != 0;
         if (!again) break;
     }
     if (again) {
-        const rsrc_t vr = make_rsrc(static_cast<const T*>(a.v) + s.k0 * a.v_s[1] + hk * a.v_s[0], a.v_ext);
-#pragma unroll
-        for (int rb = 0; rb < RB; ++rb)
-            add_kept<T, ND>(vr, vrow, t_cut * TN, kend, a.causal ? qi[rb] + s.coff : s.nk - 1, hf, oacc[rb]);
+        const rsrc_t vr = make_rsrc(static_cast<const float*>(a.v) + s.k0 * a.v_s[1] + hk * a.v_s[0], a.v_ext);
+        add_kept<float, ND>(vr, vrow, t_cut * TN, kend, a.causal ? qi + s.coff : s.nk - 1, hf, oacc);
     }
-
-#pragma unroll
-    for (int rb = 0; rb < RB; ++rb) {
-        const bool ok = qi[rb] < s.nq;
-        const float sum = l[rb] + __shfl_xor(l[rb], 32);
-        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-        const uint32_t ooff = (uint32_t)((ok ? qi[rb] : 0) * a.o_s[1] * SZ);
-#pragma unroll
-        for (int d = 0; d < ND; ++d) {
-            float x[16];
-#pragma unroll
-            for (int r = 0; r < 16; ++r) x[r] = oacc[rb][d][r] * inv;
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                if (a.o_vec) store8<T, true>(orr, ooff, ok, 32 * d + 16 * c + 8 * hf, D, x + 8 * c);
-                else store8<T, false>(orr, ooff, ok, 32 * d + 16 * c + 8 * hf, D, x + 8 * c);
-            }
-        }
-        const float lse = sum == 0.0f ? -INFINITY : (m[rb] + __builtin_amdgcn_logf(sum)) * LN2;
-        __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, lse), lr,
-                                              pred(ok && hf == 0, (uint32_t)((ok ? qi[rb] : 0) * a.l_s[1] * 4)), 0, 0);
-    }
+    store_rows<float, D>(orr, lr, a, qi, ok, hf, oacc, m, l);
 }
 
 // The same for 16-bit types, with the three parts of neighbouring 32-key
@@ -424,27 +359,27 @@ void sdpa_prompt_kernel(const PackArgs a) {
 // tile each, and join their sums at the end: for calls whose blocks leave the
 // chip's wave slots empty, the chain of tiles is half as long.
 template <typename T, int D, int NG>
-struct WideCfg {
-    static constexpr int NW = 4, RB = 1, TN = 64;
+struct PromptCfg {
+    static constexpr int NW = 4, TN = 64;
     using C = TwoPassCfg<T, D, NW, MASK_NONE, true, TN, true>;
-    static constexpr int QB = 32 * RB * NW;
-    static constexpr int JOIN_BYTES = NG > 1 ? NW * RB * (D / 32) * 16 * 64 * 4 : 0;  // one group's sums
+    static constexpr int QB = 32 * NW;
+    static constexpr int JOIN_BYTES = NG > 1 ? NW * (D / 32) * 16 * 64 * 4 : 0;  // one group's sums
     static constexpr int TILE_BYTES = NG * 4 * C::TILEB;
     static constexpr int LDS_BYTES = TILE_BYTES > JOIN_BYTES ? TILE_BYTES : JOIN_BYTES;
 };
 
 template <typename T, int D, int NG>
 __global__ __attribute__((amdgpu_flat_work_group_size(256 * NG, 256 * NG), amdgpu_waves_per_eu(2)))
-void sdpa_prompt_wide_kernel(const PackArgs a) {
-    using P = WideCfg<T, D, NG>;
+void sdpa_prompt_kernel(const PackArgs a) {
+    using P = PromptCfg<T, D, NG>;
     using C = typename P::C;
     using TR = Tr<T>;
     using vec = typename TR::vec;
-    constexpr int SZ = 2, RB = P::RB, NW = P::NW, TN = P::TN, ND = D / 32, NKS = D / 16;
-    constexpr int SLOTS = RB * NKS, EPS = 16 * RB / SLOTS;  // products of each kind in a step; exponentials per slot
+    constexpr int SZ = 2, NW = P::NW, TN = P::TN, ND = D / 32, NKS = D / 16;
+    constexpr int EPS = 16 / NKS;  // exponentials beside each of a step's products
     __shared__ __attribute__((aligned(16))) uint8_t smem[P::LDS_BYTES];
+    __shared__ float2 ml_s[NG > 1 ? NW * 64 : 1];
 
-    __shared__ float2 ml_s[NG > 1 ? NW * 64 * RB : 1];
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) % NW;
     const int grp = NG > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 8) : 0;
     uint8_t* const buf = smem + grp * 4 * C::TILEB;  // this group's tiles
@@ -484,21 +419,17 @@ void sdpa_prompt_wide_kernel(const PackArgs a) {
     auto load_k = [&](int u) SDPA_INLINE { load_tile(kd, lds + (u & 1) * C::TILEB, tile(u), kvo, krow); };
     auto load_v = [&](int u) SDPA_INLINE { load_tile(vd, lds + (2 + (u & 1)) * C::TILEB, tile(u), vvo, vrow); };
 
-    const int qw = q0 + wave * 32 * RB;  // this wave's first row
-    vec qf[RB][NKS];
+    const int qw = q0 + wave * 32, qi = qw + n;  // this wave's first row; this lane's
+    const bool ok = qi < s.nq;
+    vec qf[NKS];
+    const uint32_t qoff = (uint32_t)((ok ? qi : 0) * a.q_s[1] * SZ);
+    uint32_t qo[NKS];
 #pragma unroll
-    for (int rb = 0; rb < RB; ++rb) {
-        const int qi = qw + 32 * rb + n;
-        const bool ok = qi < s.nq;
-        const uint32_t qoff = (uint32_t)((ok ? qi : 0) * a.q_s[1] * SZ);
-        uint32_t off[NKS];
-#pragma unroll
-        for (int c = 0; c < NKS; ++c) off[c] = pred(ok, qoff + (c * 16 + hf * 8) * SZ);
-        load_operands<T, NKS>(qr, off, a.q_mul, qf[rb]);
-    }
-    f32x16 oacc[RB][ND], sc[2][RB];  // sc[j & 1]: scores of block j
-    vec pv[2][RB][2];                // pv[j & 1]: weights of block j
-    float m[RB], l[RB];
+    for (int c = 0; c < NKS; ++c) qo[c] = pred(ok, qoff + (c * 16 + hf * 8) * SZ);
+    load_operands<T, NKS>(qr, qo, a.q_mul, qf);
+    f32x16 oacc[ND], sc[2];  // sc[j & 1]: scores of block j
+    vec pv[2][2];            // pv[j & 1]: weights of block j
+    float m, l;
     const int kr0 = swap23(n);
     const int trg = lane >> 4, trs = lane & 15;
     const int tr_row = 8 * (trg >> 1) + (trs >> 2);
@@ -533,92 +464,78 @@ void sdpa_prompt_wide_kernel(const PackArgs a) {
         if constexpr (PV)
 #pragma unroll
             for (int c = 0; c < (AHEAD < 2 * ND ? AHEAD : 2 * ND); ++c) va[c] = v_op(vt, VH, c / ND, c % ND);
-        float mu[RB], sum[RB] = {};
+        float mu, sum = 0.0f;
         if constexpr (EXP) {
-            if (edge)
+            if (edge) {
+                const int lim = min(s.nk - 1 - 32 * j, a.causal ? qi + s.coff - 32 * j : 0x7fffffff) - 8 * hf;
 #pragma unroll
-                for (int rb = 0; rb < RB; ++rb) {
-                    const int qi = qw + 32 * rb + n;
-                    const int lim = min(s.nk - 1 - 32 * j, a.causal ? qi + s.coff - 32 * j : 0x7fffffff) - 8 * hf;
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) sc[PAR][rb][r] = kk(0, r) > lim ? -INFINITY : sc[PAR][rb][r];
-                }
-#pragma unroll
-            for (int rb = 0; rb < RB; ++rb) mu[rb] = m[rb] == -INFINITY ? 0.0f : -m[rb];
+                for (int r = 0; r < 16; ++r) sc[PAR][r] = kk(0, r) > lim ? -INFINITY : sc[PAR][r];
+            }
+            mu = m == -INFINITY ? 0.0f : -m;
         }
-        if constexpr (QK)
-#pragma unroll
-            for (int rb = 0; rb < RB; ++rb) sc[1 - PAR][rb] = f32x16{};
+        if constexpr (QK) sc[1 - PAR] = f32x16{};
         __builtin_amdgcn_sched_barrier(0);
-        // weights r8 .. r8 + 7 of row block rb
-        auto weights8 = [&](int rb, int r8, const float* p) SDPA_INLINE {
+        // weights r8 .. r8 + 7 of the block
+        auto weights8 = [&](int r8, const float* p) SDPA_INLINE {
             // opaque: the compiler would carry the eight floats into the next step and round them there
             u32x4 b = __builtin_bit_cast(u32x4, TR::cvt8(p));
             asm volatile("" : "+v"(b));
-            pv[PAR][rb][r8 >> 3] = as_vec<T>(b);
+            pv[PAR][r8 >> 3] = as_vec<T>(b);
         };
-        float p[16 * RB];
+        float p[16];
 #pragma unroll
-        for (int i = 0; i < SLOTS; ++i) {
-            const int rb = i % RB, c = i / RB;
+        for (int c = 0; c < NKS; ++c) {
             if constexpr (QK) {
-                sc[1 - PAR][rb] = TR::mfma(ka[c], qf[rb][c], sc[1 - PAR][rb]);
-                if (rb == 0 && c + AHEAD < NKS) ka[c + AHEAD] = k_op(kt, KH, c + AHEAD);
+                sc[1 - PAR] = TR::mfma(ka[c], qf[c], sc[1 - PAR]);
+                if (c + AHEAD < NKS) ka[c + AHEAD] = k_op(kt, KH, c + AHEAD);
             }
             if constexpr (PV) {
-                oacc[rb][c % ND] = TR::mfma(va[c], pv[1 - PAR][rb][c / ND], oacc[rb][c % ND]);
-                if (rb == RB - 1 && c + AHEAD < 2 * ND) va[c + AHEAD] = v_op(vt, VH, (c + AHEAD) / ND, (c + AHEAD) % ND);
+                oacc[c % ND] = TR::mfma(va[c], pv[1 - PAR][c / ND], oacc[c % ND]);
+                if (c + AHEAD < 2 * ND) va[c + AHEAD] = v_op(vt, VH, (c + AHEAD) / ND, (c + AHEAD) % ND);
             }
             if constexpr (EXP) {
 #pragma unroll
-                for (int e = i * EPS; e < (i + 1) * EPS; ++e) {
-                    p[e] = fast_exp2(__builtin_fmaf(sc[PAR][e >> 4][e & 15], a.scale_log2, mu[e >> 4]));
-                    sum[e >> 4] += p[e];
-                    if (e % 8 == 7) weights8(e >> 4, e & 8, p + (e & ~7));
+                for (int e = c * EPS; e < (c + 1) * EPS; ++e) {
+                    p[e] = fast_exp2(__builtin_fmaf(sc[PAR][e], a.scale_log2, mu));
+                    sum += p[e];
+                    if (e % 8 == 7) weights8(e & 8, p + (e & ~7));
                 }
             }
             __builtin_amdgcn_sched_barrier(0);
         }
         if constexpr (EXP) {
             // a sum past 2^12, or no reference yet: raise it and take block j again
-            bool grow = false;
+            if (__builtin_amdgcn_ballot_w64(sum > 4096.0f || m == -INFINITY) != 0) {
+                const f32x16& x = sc[PAR];
+                float top = x[0];
 #pragma unroll
-            for (int rb = 0; rb < RB; ++rb) grow = grow || sum[rb] > 4096.0f || m[rb] == -INFINITY;
-            if (__builtin_amdgcn_ballot_w64(grow) != 0) {
+                for (int r = 1; r < 16; ++r) top = fmaxf(top, x[r]);
+                top *= a.scale_log2;
+                const float up = fmaxf(m, fmaxf(top, __shfl_xor(top, 32)));
+                const float f = up == -INFINITY ? 1.0f : fast_exp2(m - up);
+                m = up;
+                l *= f;
 #pragma unroll
-                for (int rb = 0; rb < RB; ++rb) {
-                    const f32x16& x = sc[PAR][rb];
-                    float top = x[0];
+                for (int d = 0; d < ND; ++d)
 #pragma unroll
-                    for (int r = 1; r < 16; ++r) top = fmaxf(top, x[r]);
-                    top *= a.scale_log2;
-                    const float up = fmaxf(m[rb], fmaxf(top, __shfl_xor(top, 32)));
-                    const float f = up == -INFINITY ? 1.0f : fast_exp2(m[rb] - up);
-                    m[rb] = up;
-                    l[rb] *= f;
+                    for (int r = 0; r < 16; ++r) oacc[d][r] *= f;
+                const float nm = up == -INFINITY ? 0.0f : -up;
+                sum = 0.0f;
 #pragma unroll
-                    for (int d = 0; d < ND; ++d)
-#pragma unroll
-                        for (int r = 0; r < 16; ++r) oacc[rb][d][r] *= f;
-                    const float nm = up == -INFINITY ? 0.0f : -up;
-                    sum[rb] = 0.0f;
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) {
-                        p[r] = fast_exp2(__builtin_fmaf(x[r], a.scale_log2, nm));
-                        sum[rb] += p[r];
-                        if (r % 8 == 7) weights8(rb, r & 8, p + (r & ~7));
-                    }
+                for (int r = 0; r < 16; ++r) {
+                    p[r] = fast_exp2(__builtin_fmaf(x[r], a.scale_log2, nm));
+                    sum += p[r];
+                    if (r % 8 == 7) weights8(r & 8, p + (r & ~7));
                 }
             }
-#pragma unroll
-            for (int rb = 0; rb < RB; ++rb) l[rb] += sum[rb];
+            l += sum;
         }
     };
     static_assert(2 * ND == NKS, "as many V as K operands in a step");
 
     // tiles before t_full hold kept keys only, for every row of the wave;
     // tiles from t_end on none
-    const int last_row = min(qw + 32 * RB, s.nq) - 1;
+    const int last_row = min(qw + 32, s.nq) - 1;
     const bool live = qw < s.nq;
     const int t_end = !live ? 0 : a.causal ? max(0, min(ntiles, (last_row + s.coff + TN) / TN)) : ntiles;
     const int t_full = min(t_end, (a.causal ? max(0, min(s.nk, qw + s.coff + 1)) : s.nk) / TN);
@@ -626,11 +543,11 @@ void sdpa_prompt_wide_kernel(const PackArgs a) {
     constexpr std::integral_constant<int, 1> odd{};
     constexpr std::true_type on{};
     constexpr std::false_type off{};
-    // iteration u of the group's tiles: K tile u and V tile u - 1 are staged;
-    // the second half of tile u - 1 and the first of tile u are taken
     // the first tile with a key that some row of the workgroup does not keep
     const int t_cut = (a.causal ? max(0, min(s.nk, q0 + s.coff + 1)) : s.nk) / TN;
     bool again = false;
+    // iteration u of the group's tiles: K tile u and V tile u - 1 are staged;
+    // the second half of tile u - 1 and the first of tile u are taken
     auto stage = [&](int u) SDPA_INLINE {
         wait_copies<0>();
         __syncthreads();
@@ -644,16 +561,13 @@ void sdpa_prompt_wide_kernel(const PackArgs a) {
     };
     auto kt = [&](int u) SDPA_INLINE -> const uint8_t* { return buf + (u & 1) * C::TILEB; };
     auto vt = [&](int u) SDPA_INLINE -> const uint8_t* { return buf + (2 + ((u - 1) & 1)) * C::TILEB; };
-    const int u_all = (ntiles + NG - 1) / NG;                               // iterations of the longest group
+    const int u_all = (ntiles + NG - 1) / NG;  // iterations of the longest group
     const int u_end = NG == 1 ? t_end : t_end > grp ? (t_end - grp + NG - 1) / NG : 0;  // this wave's tiles
     for (;;) {
+        m = -INFINITY;
+        l = 0.0f;
 #pragma unroll
-        for (int rb = 0; rb < RB; ++rb) {
-            m[rb] = -INFINITY;
-            l[rb] = 0.0f;
-#pragma unroll
-            for (int d = 0; d < ND; ++d) oacc[rb][d] = f32x16{};
-        }
+        for (int d = 0; d < ND; ++d) oacc[d] = f32x16{};
         if (tile(0) < ntiles) load_k(0);
         int u = 0;
         if (u_end > 0) {
@@ -672,100 +586,61 @@ void sdpa_prompt_wide_kernel(const PackArgs a) {
         }
         for (; u <= u_all; ++u) stage(u);
         if (again || t_cut >= ntiles) break;
-        bool ok = true;
-#pragma unroll
-        for (int rb = 0; rb < RB; ++rb) ok = ok && all_finite<ND>(oacc[rb]);
-        again = __syncthreads_or(!ok) != 0;
+        again = __syncthreads_or(!all_finite<ND>(oacc)) != 0;
         if (!again) break;
     }
 
     if constexpr (NG > 1) {  // the second group's sums, then the first's join them
-        float* const js = reinterpret_cast<float*>(smem) + wave * RB * ND * 16 * 64 + lane;
+        float* const js = reinterpret_cast<float*>(smem) + wave * ND * 16 * 64 + lane;
         __syncthreads();
         if (grp == 1) {
-#pragma unroll
-            for (int rb = 0; rb < RB; ++rb) {
-                ml_s[(wave * RB + rb) * 64 + lane] = make_float2(m[rb], l[rb]);
-#pragma unroll
-                for (int d = 0; d < ND; ++d)
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) js[((rb * ND + d) * 16 + r) * 64] = oacc[rb][d][r];
-            }
-        }
-        __syncthreads();
-        if (grp == 1) return;
-#pragma unroll
-        for (int rb = 0; rb < RB; ++rb) {
-            const float2 o = ml_s[(wave * RB + rb) * 64 + lane];
-            const float up = fmaxf(m[rb], o.x);
-            const float f0 = m[rb] == -INFINITY ? 0.0f : fast_exp2(m[rb] - up), f1 = o.x == -INFINITY ? 0.0f : fast_exp2(o.x - up);
-            m[rb] = up;
-            l[rb] = l[rb] * f0 + o.y * f1;
+            ml_s[wave * 64 + lane] = make_float2(m, l);
 #pragma unroll
             for (int d = 0; d < ND; ++d)
 #pragma unroll
-                for (int r = 0; r < 16; ++r)
-                    oacc[rb][d][r] = oacc[rb][d][r] * f0 + js[((rb * ND + d) * 16 + r) * 64] * f1;
+                for (int r = 0; r < 16; ++r) js[(d * 16 + r) * 64] = oacc[d][r];
         }
+        __syncthreads();
+        if (grp == 1) return;
+        const float2 o = ml_s[wave * 64 + lane];
+        const float up = fmaxf(m, o.x);
+        const float f0 = m == -INFINITY ? 0.0f : fast_exp2(m - up), f1 = o.x == -INFINITY ? 0.0f : fast_exp2(o.x - up);
+        m = up;
+        l = l * f0 + o.y * f1;
+#pragma unroll
+        for (int d = 0; d < ND; ++d)
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+                oacc[d][r] = oacc[d][r] * f0 + js[(d * 16 + r) * 64] * f1;
     }
     if (again) {
         const rsrc_t vr = make_rsrc(static_cast<const T*>(a.v) + s.k0 * a.v_s[1] + hk * a.v_s[0], a.v_ext);
-#pragma unroll
-        for (int rb = 0; rb < RB; ++rb)
-            add_kept<T, ND>(vr, vrow, t_cut * TN, kend, a.causal ? qw + 32 * rb + n + s.coff : s.nk - 1, hf, oacc[rb]);
+        add_kept<T, ND>(vr, vrow, t_cut * TN, kend, a.causal ? qi + s.coff : s.nk - 1, hf, oacc);
     }
-#pragma unroll
-    for (int rb = 0; rb < RB; ++rb) {
-        const int qi = qw + 32 * rb + n;
-        const bool ok = qi < s.nq;
-        const float sum = l[rb] + __shfl_xor(l[rb], 32);
-        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-        const uint32_t ooff = (uint32_t)((ok ? qi : 0) * a.o_s[1] * SZ);
-#pragma unroll
-        for (int d = 0; d < ND; ++d) {
-            float x[16];
-#pragma unroll
-            for (int r = 0; r < 16; ++r) x[r] = oacc[rb][d][r] * inv;
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                if (a.o_vec) store8<T, true>(orr, ooff, ok, 32 * d + 16 * c + 8 * hf, D, x + 8 * c);
-                else store8<T, false>(orr, ooff, ok, 32 * d + 16 * c + 8 * hf, D, x + 8 * c);
-            }
-        }
-        const float lse = sum == 0.0f ? -INFINITY : (m[rb] + __builtin_amdgcn_logf(sum)) * LN2;
-        __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, lse), lr,
-                                              pred(ok && hf == 0, (uint32_t)((ok ? qi : 0) * a.l_s[1] * 4)), 0, 0);
-    }
+    store_rows<T, D>(orr, lr, a, qi, ok, hf, oacc, m, l);
 }
 
-template <typename T>
+template <typename T, int NG>
 static int launch_prompt_t(int D, const PackArgs& a, hipStream_t s) {
-    const dim3 grid((uint32_t)a.B * a.Hq * a.n_blk);
-#define SDPA_PROMPT_D(KERNEL, THREADS, ...)                                            \
-    switch (D) {                                                                       \
-        case 32: KERNEL<T, 32, ##__VA_ARGS__><<<grid, THREADS, 0, s>>>(a); break;      \
-        case 64: KERNEL<T, 64, ##__VA_ARGS__><<<grid, THREADS, 0, s>>>(a); break;      \
-        case 128: KERNEL<T, 128, ##__VA_ARGS__><<<grid, THREADS, 0, s>>>(a); break;    \
-        default: return (int)hipErrorInvalidValue;                                     \
+    const dim3 grid((uint32_t)a.B * a.Hq * a.n_blk), block(256 * NG);
+#define SDPA_PROMPT(D)                                                                   \
+    if constexpr (sizeof(T) == 4) sdpa_prompt_f32_kernel<D><<<grid, block, 0, s>>>(a);   \
+    else sdpa_prompt_kernel<T, D, NG><<<grid, block, 0, s>>>(a);
+    switch (D) {
+        case 32: SDPA_PROMPT(32) break;
+        case 64: SDPA_PROMPT(64) break;
+        case 128: SDPA_PROMPT(128) break;
+        default: return (int)hipErrorInvalidValue;
     }
-    if constexpr (sizeof(T) == 4) {
-        SDPA_PROMPT_D(sdpa_prompt_kernel, 256)
-    } else if (a.groups == 2) {
-        SDPA_PROMPT_D(sdpa_prompt_wide_kernel, 512, 2)
-    } else {
-        SDPA_PROMPT_D(sdpa_prompt_wide_kernel, 256, 1)
-    }
-#undef SDPA_PROMPT_D
+#undef SDPA_PROMPT
     return (int)hipGetLastError();
 }
 
 int launch_prompt(int dtype, int D, const PackArgs& a, void* stream) {
     hipStream_t s = static_cast<hipStream_t>(stream);
-    switch (dtype) {
-        case DT_F32: return launch_prompt_t<float>(D, a, s);
-        case DT_F16: return launch_prompt_t<_Float16>(D, a, s);
-        default: return launch_prompt_t<__bf16>(D, a, s);
-    }
+    if (dtype == DT_F32) return launch_prompt_t<float, 1>(D, a, s);
+    if (dtype == DT_F16) return a.groups == 2 ? launch_prompt_t<_Float16, 2>(D, a, s) : launch_prompt_t<_Float16, 1>(D, a, s);
+    return a.groups == 2 ? launch_prompt_t<__bf16, 2>(D, a, s) : launch_prompt_t<__bf16, 1>(D, a, s);
 }
 
 // ------------------------------------------------------------------ key weights

@@ -88,9 +88,9 @@ def prompt(q, k, v, cu_q, cu_k, causal=True, align="top_left", scale=None):
             lse[a:z, h] = L
             to[a:z, h] = u(q.dtype) * torch.nan_to_num(o[a:z, h], 0.0, 0.0, 0.0).abs() + ((up + sl) * (1 + u(q.dtype)))[:, None] * A + 1e-30
             if q.dtype == torch.float16:
-                # fp16 probabilities below 2^-14 and results near 0 round to steps of 2^-24; a row's largest
-                # probability is taken as 1/2 at least (its reference is rounded up to a whole power of two)
-                to[a:z, h] += 2.0 ** -25 * (1 + 2 * (p > 0).double() @ torch.nan_to_num(vv.abs(), 0.0, 0.0, 0.0))
+                # fp16 probabilities below 2^-14 and results near 0 round to steps of 2^-24; a row's reference is the
+                # maximum of some of its scores, so its probabilities are taken with a sum of 1 at least
+                to[a:z, h] += 2.0 ** -25 * (1 + (p > 0).double() @ torch.nan_to_num(vv.abs(), 0.0, 0.0, 0.0))
             tl[a:z, h] = sl + 2.0 ** -22 * torch.nan_to_num(L, 0.0, 0.0, 0.0).abs()
     return o, lse, to, tl
 
