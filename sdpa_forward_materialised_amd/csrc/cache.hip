@@ -733,16 +733,19 @@ int launch_cache_attention(int dtype, const CacheArgs& a, void* stream) {
 //
 // sdpa_cache_select_kernel: one workgroup per (sequence, key head) finds the
 // tokens to keep. The weights of the candidates (the tokens before the recent
-// ones) become integers of the same order (NaN highest), kept in LDS where
-// they fit; a radix histogram of 11, 11 and 10 bits gives the value of the last
-// candidate kept. Its first part is taken while the weights are loaded; then
-// one pass marks what is above the bits found, as bits of a word for every 64
-// tokens, and lists what shares them (few, unless many weights are nearly
-// equal: then every pass goes over all), and the rest goes by the list. After a
-// scan over the waves' counts each wave emits its kept tokens in order, of
-// those tied with the last the first. Counts are integers and the list's order
-// has no effect, so the atomics leave nothing to chance. One CU's instructions
-// bound it: 32768 tokens 30 us, 4096 12 (MI355X).
+// ones) become integers of the same order (NaN highest), counted from the
+// smallest of them, so that the highest 11 bits of their range tell many of
+// them apart: a histogram of those gives the bin that holds the last candidate
+// kept. A bin of at most SELECT_LIST tokens is listed and one wave finds the
+// value bit by bit with ballots; a longer one (many weights nearly equal) is
+// taken apart by further histograms. After a scan over the waves' counts each
+// wave emits its kept tokens in order, of those tied with the last the first.
+// Counts are integers and the list's order has no effect, so the atomics leave
+// nothing to chance. The integers stay in registers, 64 a thread, which is
+// enough for 65536 candidates; beyond that every pass reads the weights again
+// (an eviction of 8 heads of 65536 tokens takes 127 us so, 70 with registers).
+// One CU bounds it, its loads (28 % of 32768 tokens' time), LDS atomics (23 %)
+// and the ordered stores: 32768 tokens 25 us, 4096 9.8 (MI355X).
 __device__ __forceinline__ uint32_t order_key(float x) {
     const uint32_t u = __builtin_bit_cast(uint32_t, x);
     const uint32_t k = u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);  // negative: all bits turn, else the sign
@@ -755,19 +758,47 @@ __device__ __forceinline__ float key_value(uint32_t k) {
 }
 
 constexpr int SELECT_THREADS = 1024;
-constexpr int SELECT_LIST = 1024;
+constexpr int SELECT_LIST = 256;
+constexpr int SELECT_WORDS = 64;
 
-// CAP: candidates whose keys LDS holds, a multiple of 4096 (0: any number,
-// read again from memory).
-template <int CAP>
+// all lanes of a row of 16 get the row's smallest / largest
+template <bool MAX>
+__device__ __forceinline__ uint32_t row_extreme(uint32_t x) {
+    auto with = [&](uint32_t y) SDPA_INLINE { x = MAX ? max(x, y) : min(x, y); };
+    with(__builtin_amdgcn_update_dpp(x, x, 0x128, 0xf, 0xf, false));  // rotated by 8, 4, 2, 1
+    with(__builtin_amdgcn_update_dpp(x, x, 0x124, 0xf, 0xf, false));
+    with(__builtin_amdgcn_update_dpp(x, x, 0x122, 0xf, 0xf, false));
+    with(__builtin_amdgcn_update_dpp(x, x, 0x121, 0xf, 0xf, false));
+    return x;
+}
+template <bool MAX>
+__device__ __forceinline__ uint32_t wave_extreme(uint32_t x) {
+    const int y = (int)row_extreme<MAX>(x);
+    uint32_t z = (uint32_t)__builtin_amdgcn_readlane(y, 0);
+#pragma unroll
+    for (int r = 16; r < 64; r += 16) {
+        const uint32_t o = (uint32_t)__builtin_amdgcn_readlane(y, r);
+        z = MAX ? max(z, o) : min(z, o);
+    }
+    return z;
+}
+
+// f(4 i) for every i below words / 4 (N at most), unrolled
+template <int... I, typename F>
+__device__ __forceinline__ void by_four(std::integer_sequence<int, I...>, int words, F f) {
+    (void)((4 * I < words && (f(std::integral_constant<int, 4 * I>{}), true)) && ...);
+}
+
+// WORDS: 64-token words whose integers a wave keeps in registers, a multiple of
+// 4 (0: any number, read again from memory).
+template <int WORDS>
 __global__ __attribute__((amdgpu_flat_work_group_size(SELECT_THREADS, SELECT_THREADS)))
 void sdpa_cache_select_kernel(const CacheArgs a) {
     constexpr int NT = SELECT_THREADS, NWV = NT / 64, NB = 2048;
-    constexpr int WORDS = CAP > 0 ? CAP / 64 : 1;
-    __shared__ __attribute__((aligned(16))) uint32_t keys[CAP > 0 ? CAP : 1];
-    __shared__ uint64_t kept_bits[WORDS], tied_bits[WORDS];
+    static_assert(NWV == 16, "the waves' extremes fit one row of lanes");
     __shared__ int hist[NB];
-    __shared__ uint2 list[SELECT_LIST];  // key, token
+    __shared__ uint32_t list[SELECT_LIST];
+    __shared__ uint32_t lo_s[NWV], hi_s[NWV];
     __shared__ int wsum[NWV], wtie[NWV];
     __shared__ int pick_s, above_s, bin_s, list_n;
     const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -779,104 +810,135 @@ void sdpa_cache_select_kernel(const CacheArgs a) {
     const float* w = a.w_in + b * a.wi_s[0] + h * a.wi_s[1];
     float* wo = a.w_out + b * a.wo_s[0] + h * a.wo_s[1];
     int* kept = a.kept + ((int64_t)b * a.Hkv + h) * a.budget;
-    const bool some = take > 0 && take < late;
     // a wave's stretch: `words` words of 64 tokens, a multiple of 4
     const int words = ((late + 4 * NT - 1) / (4 * NT)) * 4;
     const int t0 = wave * words * 64 + lane;
 
-    auto clear = [&]() SDPA_INLINE {
-        for (int i = tid; i < NB; i += NT) hist[i] = 0;
-    };
-    // one more token in bin `bin` for every lane with `in` (all lanes call)
-    auto add = [&](int bin, bool in) SDPA_INLINE {
-        const uint64_t who = __builtin_amdgcn_ballot_w64(in);
-        if (who == 0) return;
-        const int first = __builtin_amdgcn_readlane(bin, __builtin_ctzll(who));
-        if (__builtin_amdgcn_ballot_w64(in && bin != first) == 0) {  // one bin (equal weights): one addition
-            if (lane == 0) atomicAdd(&hist[first], __popcll(who));
-        } else if (in) {
-            atomicAdd(&hist[bin], 1);
-        }
-    };
-    // keys of the words i .. i + 3 of this wave; no candidate has key 0
-    auto four = [&](int i, uint32_t* k) SDPA_INLINE {
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int j = t0 + 64 * (i + e);
-            if constexpr (CAP > 0) k[e] = keys[j];
-            else k[e] = j < late ? order_key(w[j]) : 0u;
-        }
-    };
     float recent[4];  // the first recent weights, in flight behind all that follows
-    if constexpr (CAP > 0) {
+    if constexpr (WORDS > 0) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) recent[e] = e * NT + tid < len - late ? w[late + e * NT + tid] : 0.0f;
     }
-    clear();
-    if (tid == 0) list_n = 0;
-    __syncthreads();
-    for (int i = 0; i < words; i += 16) {  // every key, and the histogram of the highest bits
-        float x[16];
-        const int m = min(16, words - i);
+    constexpr std::make_integer_sequence<int, WORDS / 4> quads{};
+    uint32_t key[WORDS > 0 ? WORDS : 1] = {};
+    uint32_t base = 0;  // what `each` takes from the integers
+    // f(word, integer) for this wave's words in order; no candidate has integer 0, all else has
+    auto each = [&](auto f) SDPA_INLINE {
+        if constexpr (WORDS > 0) {
+            by_four(quads, words, [&](auto i) SDPA_INLINE {
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-            const int j = t0 + 64 * (i + e);
-            x[e] = e < m && j < late ? w[j] : 0.0f;
-        }
+                for (int e = 0; e < 4; ++e) f(i + e, key[i + e]);
+            });
+        } else {
+            for (int i = 0; i < words; i += 4) {
+                uint32_t k[4];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-            if (e >= m) break;
-            const int j = t0 + 64 * (i + e);
-            const uint32_t k = j < late ? order_key(x[e]) : 0u;
-            if constexpr (CAP > 0) keys[j] = k;
-            if (some) add((int)(k >> 21), j < late);
+                for (int e = 0; e < 4; ++e) {
+                    const int j = t0 + 64 * (i + e);
+                    k[e] = j < late ? order_key(w[j]) - base : 0u;
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) f(i + e, k[e]);
+            }
         }
+    };
+    if constexpr (WORDS > 0) {
+        const rsrc_t wr = make_rsrc(w, (uint32_t)late * 4);
+        by_four(quads, words, [&](auto i) SDPA_INLINE {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) key[i + e] = (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(wr, 4 * (t0 + 64 * (i + e)), 0, 0);
+        });
+        int end = late;  // opaque: the comparisons are made again, rather than kept for every word
+        asm volatile("" : "+s"(end));
+        by_four(quads, words, [&](auto i) SDPA_INLINE {
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                key[i + e] = t0 + 64 * (i + e) < end ? order_key(__builtin_bit_cast(float, key[i + e])) : 0u;
+        });
     }
     // the largest `pick` that `take` candidates reach, and how many of those equal to it are kept
-    uint32_t pick = 0;
-    int need = take;
-    bool listed = false;
-    if (some) {
-        uint32_t mask = 0;
-        for (int pass = 0; pass < 3; ++pass) {
-            const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1024 : 2048;
-            if (pass > 0) {
-                clear();
-                if (pass == 1) {
-                    listed = CAP > 0 && bin_s <= SELECT_LIST;  // bin_s: tokens that share the first 11 bits
-                    if (listed) {
-                        // mark what is above these bits, and list what shares them
-                        for (int i = 0; i < words; i += 4) {
-                            uint32_t k[4];
-                            four(i, k);
+    uint32_t pick = take == 0 ? 0xffffffffu : 0u;  // none, or every candidate
+    int need = 0;
+    if (take > 0 && take < late) {
+        auto clear = [&]() SDPA_INLINE {
+            for (int i = tid; i < NB; i += NT) hist[i] = 0;
+        };
+        // one more token in bin `bin` for every lane with `in` (all lanes call)
+        auto add = [&](int bin, bool in) SDPA_INLINE {
+            const uint64_t who = __builtin_amdgcn_ballot_w64(in);
+            if (who == 0) return;
+            const int first = __builtin_amdgcn_readlane(bin, __builtin_ctzll(who));
+            if (__builtin_amdgcn_ballot_w64(in && bin != first) == 0) {  // one bin (equal weights): one addition
+                if (lane == 0) atomicAdd(&hist[first], __popcll(who));
+            } else if (in) {
+                atomicAdd(&hist[bin], 1);
+            }
+        };
+        clear();
+        if (tid == 0) list_n = 0;
+        uint32_t lo = 0xffffffffu, hi = 0;
+        each([&](int, uint32_t k) SDPA_INLINE {
+            lo = min(lo, k - 1);  // 0 counts as the largest
+            hi = max(hi, k);
+        });
+        lo = wave_extreme<false>(lo);
+        hi = wave_extreme<true>(hi);
+        if (lane == 0) {
+            lo_s[wave] = lo;
+            hi_s[wave] = hi;
+        }
+        __syncthreads();
+        base = __builtin_amdgcn_readfirstlane((int)row_extreme<false>(lo_s[lane & 15]));
+        // integers are 1 .. hi - base now, of `rem` bits that `pick` lacks
+        int rem = 32 - __builtin_clz(__builtin_amdgcn_readfirstlane((int)row_extreme<true>(hi_s[lane & 15])) - base);
+        if constexpr (WORDS > 0) {
+            by_four(quads, words, [&](auto i) SDPA_INLINE {
 #pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const bool in = (k[e] & mask) == pick;
-                                const uint64_t kb = __builtin_amdgcn_ballot_w64((k[e] & mask) > pick);
-                                if (lane == 0) {
-                                    kept_bits[wave * words + i + e] = kb;
-                                    tied_bits[wave * words + i + e] = 0;
-                                }
-                                if (in) list[atomicAdd(&list_n, 1)] = make_uint2(k[e], (uint32_t)(t0 + 64 * (i + e)));
-                            }
-                        }
+                for (int e = 0; e < 4; ++e) key[i + e] -= key[i + e] != 0 ? base : 0u;
+            });
+        }
+        need = take;
+        bool first = true;
+        while (rem > 0) {
+            if (!first && bin_s <= SELECT_LIST) {  // bin_s: tokens that share the bits found
+                uint32_t none = 0;  // opaque, as below
+                asm volatile("" : "+s"(none));
+                each([&](int, uint32_t k) SDPA_INLINE {
+                    if (k != none && k >> rem == pick >> rem) list[atomicAdd(&list_n, 1)] = k & ((1u << rem) - 1);
+                });
+                __syncthreads();
+                if (wave == 0) {
+                    uint32_t x[SELECT_LIST / 64], v = 0;
+#pragma unroll
+                    for (int e = 0; e < SELECT_LIST / 64; ++e) x[e] = lane + 64 * e < list_n ? list[lane + 64 * e] : 0u;
+                    auto reach = [&](uint32_t t) SDPA_INLINE {  // tokens of at least t > 0
+                        int c = 0;
+#pragma unroll
+                        for (int e = 0; e < SELECT_LIST / 64; ++e) c += __popcll(__builtin_amdgcn_ballot_w64(x[e] >= t));
+                        return c;
+                    };
+                    for (int bit = rem - 1; bit >= 0; --bit)
+                        if (reach(v | 1u << bit) >= need) v |= 1u << bit;
+                    if (lane == 0) {
+                        pick_s = (int)v;
+                        above_s = reach(v + 1);
                     }
                 }
                 __syncthreads();
-                if (listed) {
-                    for (int i = tid & ~63; i < list_n; i += NT) {
-                        const uint32_t k = i + lane < list_n ? list[i + lane].x : 0u;
-                        add((int)(k >> shift) & (bins - 1), (k & mask) == pick);
-                    }
-                } else {
-                    for (int i = 0; i < words; i += 4) {
-                        uint32_t k[4];
-                        four(i, k);
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) add((int)(k[e] >> shift) & (bins - 1), (k[e] & mask) == pick);
-                    }
-                }
+                pick |= (uint32_t)pick_s;
+                need -= above_s;
+                break;
             }
+            const int shift = max(rem - 11, 0);
+            if (!first) {
+                clear();
+                __syncthreads();
+            }
+            uint32_t none = 0;  // opaque: compared in every pass, rather than a mask kept for every word
+            asm volatile("" : "+s"(none));
+            each([&](int, uint32_t k) SDPA_INLINE {
+                add((int)(k >> shift) & (NB - 1), k != none && (first || k >> rem == pick >> rem));
+            });
             __syncthreads();
             // the highest bin that, with all above it, holds `need` tokens:
             // a wave sums 128 bins, from the top down over lanes and waves
@@ -897,56 +959,24 @@ void sdpa_cache_select_kernel(const CacheArgs a) {
                 const bool one = upto - c1 >= need;
                 pick_s = one ? top : top - 1;
                 above_s = one ? upto - c1 - c0 : upto - c1;
-                if (pass == 0) bin_s = one ? c0 : c1;
+                bin_s = one ? c0 : c1;
             }
             __syncthreads();
             pick |= (uint32_t)pick_s << shift;
-            mask |= (uint32_t)(bins - 1) << shift;
             need -= above_s;
+            rem = shift;
+            first = false;
         }
-    } else {
-        pick = take == 0 ? 0xffffffffu : 0u;  // none (ties count 0 below), or every candidate
-        need = 0;
-        __syncthreads();
     }
-    // mark and count
+    // count, over the waves
+    pick = (uint32_t)__builtin_amdgcn_readfirstlane((int)pick);
+    need = __builtin_amdgcn_readfirstlane(need);
     int cnt = 0, tie = 0;
-    if (listed) {
-        for (int i = tid; i < list_n; i += NT) {
-            const uint2 e = list[i];
-            if (e.x < pick) continue;
-            unsigned long long* const bits = reinterpret_cast<unsigned long long*>(e.x > pick ? kept_bits : tied_bits);
-            atomicOr(&bits[e.y >> 6], 1ull << (e.y & 63));
-        }
-        __syncthreads();
-        for (int i = lane; i < words; i += 64) {
-            cnt += __popcll(kept_bits[wave * words + i]);
-            tie += __popcll(tied_bits[wave * words + i]);
-        }
-#pragma unroll
-        for (int k = 1; k < 64; k *= 2) {
-            cnt += __shfl_xor(cnt, k);
-            tie += __shfl_xor(tie, k);
-        }
-    } else {
-        for (int i = 0; i < words; i += 4) {
-            uint32_t k[4];
-            four(i, k);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const uint64_t kb = __builtin_amdgcn_ballot_w64(k[e] > pick);
-                const uint64_t tb = __builtin_amdgcn_ballot_w64(k[e] == pick && pick != 0);
-                cnt += __popcll(kb);
-                tie += __popcll(tb);
-                if constexpr (CAP > 0) {
-                    if (lane == 0) {
-                        kept_bits[wave * words + i + e] = kb;
-                        tied_bits[wave * words + i + e] = tb;
-                    }
-                }
-            }
-        }
-    }
+    each([&](int, uint32_t k) SDPA_INLINE {
+        cnt += __popcll(__builtin_amdgcn_ballot_w64(k > pick));
+        tie += __popcll(__builtin_amdgcn_ballot_w64(k == pick));
+    });
+    __syncthreads();
     if (lane == 0) {
         wsum[wave] = cnt;
         wtie[wave] = tie;
@@ -957,49 +987,50 @@ void sdpa_cache_select_kernel(const CacheArgs a) {
         at += wsum[i] + min(ties + wtie[i], need) - min(ties, need);
         ties += wtie[i];
     }
+    asm volatile("" : "+s"(pick));  // opaque: compared again, rather than every word's two masks kept
     const uint64_t below = (uint64_t(1) << lane) - 1;
-    for (int i0 = 0; i0 < words; i0 += 4) {
-        uint64_t kb[4], tb[4];
-        uint32_t k[4];
-        four(i0, k);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            if constexpr (CAP > 0) {
-                kb[e] = kept_bits[wave * words + i0 + e];
-                tb[e] = tied_bits[wave * words + i0 + e];
+    const rsrc_t kr = make_rsrc(kept, 4 * (uint32_t)max(take, 0)), wor = make_rsrc(wo, 4 * (uint32_t)max(take, 0));
+    each([&](int i, uint32_t k) SDPA_INLINE {
+        uint64_t kb = __builtin_amdgcn_ballot_w64(k > pick);
+        const uint64_t tb = __builtin_amdgcn_ballot_w64(k == pick);
+        if (tb != 0) {
+            const bool tied = (tb >> lane & 1) && ties + __popcll(tb & below) < need;
+            kb |= __builtin_amdgcn_ballot_w64(tied);
+            ties += __popcll(tb);
+        }
+        if (kb >> lane & 1) {
+            const int to = at + __popcll(kb & below);
+            if constexpr (WORDS > 0) {
+                __builtin_amdgcn_raw_buffer_store_b32(t0 + 64 * i, kr, 4 * to, 0, 0);
+                // in place too: every candidate is in registers
+                __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(int, key_value(k + base)), wor, 4 * to, 0, 0);
             } else {
-                kb[e] = __builtin_amdgcn_ballot_w64(k[e] > pick);
-                tb[e] = __builtin_amdgcn_ballot_w64(k[e] == pick && pick != 0);
+                kept[to] = t0 + 64 * i;
             }
         }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            if (tb[e] != 0) {
-                const bool tied = (tb[e] >> lane & 1) && ties + __popcll(tb[e] & below) < need;
-                kb[e] |= __builtin_amdgcn_ballot_w64(tied);
-                ties += __popcll(tb[e]);
-            }
-            if (kb[e] >> lane & 1) {
-                const int to = at + __popcll(kb[e] & below);
-                kept[to] = t0 + 64 * (i0 + e);
-                if constexpr (CAP > 0) wo[to] = key_value(k[e]);  // in place too: every candidate is in LDS
-            }
-            at += __popcll(kb[e]);
-        }
-    }
+        at += __popcll(kb);
+    });
     for (int i = tid; i < len - late; i += NT) kept[take + i] = late + i;
     for (int i = n + tid; i < a.budget; i += NT) kept[i] = -1;
-    // the recent tokens' weights (or, without keys in LDS, all): a token never
-    // moves up, and each round's reads end before its writes begin, so that
-    // they may move in place
-    if constexpr (CAP == 0) __syncthreads();
-    for (int i0 = CAP > 0 ? take : 0; i0 < n; i0 += 4 * NT) {
+    // the recent tokens' weights (or, without integers in registers, all): a
+    // token never moves up, and every round's reads end before its writes
+    // begin, so that they may move in place. The first recent ones were read
+    // before the barriers above.
+    int i0 = 0;
+    if constexpr (WORDS > 0) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (e * NT + tid < len - late) wo[take + e * NT + tid] = recent[e];
+        i0 = take + 4 * NT;
+    } else {
+        __syncthreads();
+    }
+    for (; i0 < n; i0 += 4 * NT) {
         float x[4] = {};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             const int i = i0 + e * NT + tid;
-            if (CAP > 0 && i0 == take) x[e] = recent[e];
-            else x[e] = i >= n ? 0.0f : w[CAP > 0 ? late + i - take : kept[i]];
+            if (i < n) x[e] = w[WORDS > 0 ? late + i - take : kept[i]];
         }
         __syncthreads();
 #pragma unroll
@@ -1007,7 +1038,6 @@ void sdpa_cache_select_kernel(const CacheArgs a) {
             if (i0 + e * NT + tid < n) wo[i0 + e * NT + tid] = x[e];
         __syncthreads();
     }
-    __syncthreads();
     for (int i = n + tid; i < a.w_cols; i += NT) wo[i] = 0.0f;
     if (h == 0 && tid == 0) a.new_lens[b] = n;
 }
@@ -1018,15 +1048,19 @@ void sdpa_cache_select_kernel(const CacheArgs a) {
 // `page` apart, so that every cache line of a v page that keeps a token is
 // read whatever the access: these pages are staged in LDS whole (kept tokens
 // are ordered, so few pages hold them), in batches of MOVE_STAGE bytes, and
-// the tokens' columns picked there. The chain kept -> table -> scale -> page
+// the tokens' columns picked there. 16 KB a batch leave room for eight
+// workgroups a CU, which hide the loads (16 sequences of up to 4096 tokens, 8
+// heads, to 1024: 27 us, 3.6 TB/s of what it has to move; 32 KB 32 us, 64 KB
+// 45). The chain kept -> table -> scale -> page
 // of dependent loads is gone through once for k and v together, and the loads
 // of k and of the first batch of v are in flight at once.
-constexpr int MOVE_STAGE = 32 * 1024;
+template <int BYTES>
+constexpr int MOVE_STAGE = BYTES > 16 * 1024 ? BYTES : 16 * 1024;
 
 template <int D, int P>
 __global__ __attribute__((amdgpu_flat_work_group_size(256, 256)))
 void sdpa_cache_move_kernel(const CacheArgs a) {
-    __shared__ __attribute__((aligned(16))) uint8_t stage[MOVE_STAGE];
+    __shared__ __attribute__((aligned(16))) uint8_t stage[MOVE_STAGE<D * P>];
     __shared__ int src_slot[P], src_off[P], page_list[P];
     __shared__ float rk[P], rv[P];
     __shared__ float redk[2], redv[2];
@@ -1096,7 +1130,7 @@ void sdpa_cache_move_kernel(const CacheArgs a) {
         a.vs[(int64_t)to * a.Hkv + h] = top_v;
     }
     constexpr int BYTES = D * P, CHUNKS = BYTES / 16;
-    constexpr int BATCH = MOVE_STAGE / BYTES < P ? MOVE_STAGE / BYTES : P;  // v pages staged at a time
+    constexpr int BATCH = MOVE_STAGE<BYTES> / BYTES < P ? MOVE_STAGE<BYTES> / BYTES : P;  // v pages staged at a time
     constexpr int NL = (BATCH * CHUNKS + 255) / 256;                         // 16-byte loads of a thread
     constexpr int PER = D / 16, NK = (CHUNKS + 255) / 256;                   // pieces of a k row, pieces of a thread
     u32x4 kx[NK];
@@ -1181,9 +1215,7 @@ int launch_cache_evict(const CacheArgs& a, void* stream) {
     // lengths are at most the weights' row and the table's pages
     const int64_t pages = (int64_t)a.max_pages * a.page, most = a.w_cols < pages ? a.w_cols : pages;
     const dim3 grid(a.B * a.Hkv), block(SELECT_THREADS);
-    if (most <= 4096) sdpa_cache_select_kernel<4096><<<grid, block, 0, s>>>(a);
-    else if (most <= 16384) sdpa_cache_select_kernel<16384><<<grid, block, 0, s>>>(a);
-    else if (most <= 32768) sdpa_cache_select_kernel<32768><<<grid, block, 0, s>>>(a);
+    if (most <= 1024 * SELECT_WORDS) sdpa_cache_select_kernel<SELECT_WORDS><<<grid, block, 0, s>>>(a);
     else sdpa_cache_select_kernel<0><<<grid, block, 0, s>>>(a);
     int e = (int)hipGetLastError();
     if (e || a.to_pages == 0) return e;

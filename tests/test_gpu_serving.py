@@ -352,3 +352,53 @@ def test_evict(case):
     in_place = w.to(DEV)
     S.cache_evict(c, table.to(DEV), il.to(DEV), in_place, budget, recent, to.to(DEV))
     assert torch.equal(torch.nan_to_num(in_place, 7.5), torch.nan_to_num(w_out, 7.5))
+
+
+SELECT = [
+    # label, lens, budget, recent, weights
+    ("close", [6000], 700, 40, lambda g, *s: 1.0 + torch.randint(0, 2000, s, generator=g) * 2.0 ** -23),  # a full bin of the first histogram
+    ("two-scales", [9000, 3], 5000, 0, lambda g, *s: torch.where(torch.rand(*s, generator=g) < 0.5, 1e-38, 1.0) * (
+        1 + torch.randint(0, 5000, s, generator=g) * 2.0 ** -20)),
+    ("many-equal", [12000], 3000, 100, lambda g, *s: torch.randint(0, 3, s, generator=g).float()),
+    ("many-recent", [30001], 20000, 19000, lambda g, *s: torch.rand(*s, generator=g)),
+    ("recent-only-room", [5000], 4500, 4499, lambda g, *s: torch.rand(*s, generator=g)),
+    ("40000", [40000, 17], 4095, 512, lambda g, *s: torch.rand(*s, generator=g).exp2()),
+    ("65536", [65536], 65535, 1, lambda g, *s: torch.randn(*s, generator=g)),
+    ("denormal", [4097], 64, 0, lambda g, *s: torch.randint(0, 1 << 20, s, generator=g) * 2.0 ** -149),
+    ("70000", [70000, 66000, 1], 6000, 300, lambda g, *s: torch.rand(*s, generator=g)),
+    ("70000-equal", [70000], 6000, 300, lambda g, *s: torch.ones(*s)),
+    ("70000-recent", [70000], 12001, 12000, lambda g, *s: torch.rand(*s, generator=g)),
+]
+
+
+@pytest.mark.parametrize("case", SELECT, ids=[c[0] for c in SELECT])
+def test_evict_selection(case):
+    """Which tokens stay, and their weights, over many tokens: pages of no pool, so that nothing moves."""
+    S = _lib()
+    label, lens, budget, recent, draw = case
+    B, H, P = len(lens), 2, 128
+    w = draw(_gen(sum(lens)), B, H, max(lens) + 3).float()
+    pages = -(-max(lens) // P)
+    c = S.new_cache(1, H, 32, P, DEV)
+    table = torch.full((B, pages), -1, dtype=torch.int32, device=DEV)
+    to = torch.full((B, -(-budget // P)), -1, dtype=torch.int32, device=DEV)
+    want = torch.full((B, H, budget), -1, dtype=torch.int32)
+    wo = torch.zeros_like(w)
+    for b, n in enumerate(lens):
+        late = max(n - recent, 0) if n > budget else 0
+        for h in range(H):
+            order = torch.sort(w[b, h, :late], descending=True, stable=True).indices[:budget - (n - late)]
+            keep = torch.cat([order.sort().values, torch.arange(late, n)])
+            want[b, h, :len(keep)] = keep
+            wo[b, h, :len(keep)] = w[b, h, keep]
+    il = torch.tensor(lens, dtype=torch.int32).to(DEV)
+    print(f"[case] selection {label}", flush=True)
+    w_out = _nan(*w.shape)
+    kept, nl = S.cache_evict(c, table, il, w.to(DEV), budget, recent, to, weights_out=w_out)
+    in_place = w.to(DEV)
+    again, _ = S.cache_evict(c, table, il, in_place, budget, recent, to)
+    torch.cuda.synchronize()
+    _bits("kept", kept, want)
+    assert nl.tolist() == [min(n, budget) for n in lens]
+    assert torch.equal(w_out.cpu(), wo) and torch.equal(in_place.cpu(), wo)
+    assert torch.equal(again, kept)
