@@ -18,7 +18,8 @@
  * and no result depends on an order of atomics, so calls can be recorded into
  * HIP graphs and repeat bit for bit. A workspace is scratch for its call:
  * calls that share one must be ordered (two graphs with one workspace must
- * not run at once).
+ * not run at once). Lengths, page tables and rows of weights go up to 2^30
+ * tokens.
  */
 #ifndef SDPA_SERVE_H
 #define SDPA_SERVE_H
@@ -164,7 +165,7 @@ sdpa_status_t sdpa_cache_attention_workspace_bytes(const sdpa_tensor_t* q, const
  *       lengths are cut to W): weights_out holds the kept tokens' weights in
  *       order and zeros behind them
  * kept      int32 [n_seqs, Hkv, budget], contiguous: positions kept, -1 behind
- * new_lens  int32 [n_seqs]: min(length, budget)
+ * new_lens  int32 [n_seqs]: min(length, budget); not kv_lens itself, which every head reads
  */
 sdpa_status_t sdpa_cache_evict(const sdpa_cache_t* cache, const int32_t* page_table, int64_t n_seqs,
                                int64_t max_pages, int64_t table_stride, const int32_t* kv_lens,

@@ -6,7 +6,8 @@ Argument marshalling only, like the rest of the binding: workspaces and default
 outputs come from torch's caching allocator, the launch goes to torch's current
 stream on the tensors' device, and nothing here synchronises or reads device
 data. A tensor that was produced on another stream has to be ordered before the
-call by the caller, as for any torch operator.
+call by the caller, as for any torch operator. There are no gradients:
+``sdpa_math`` and ``bwd`` are for training.
 """
 
 from __future__ import annotations
@@ -65,10 +66,11 @@ class PagedCache:
     ``k`` [n_pages, Hkv, page, D] and ``v`` [n_pages, Hkv, D, page] (the tokens
     of a page innermost) hold float8_e4m3fn codes; ``k_scale`` and ``v_scale``
     [n_pages, Hkv] (float32) the power of two that a page's and head's codes are
-    multiplied with. The tensors must keep their storage while the object lives.
+    multiplied with. The object holds these tensors for good (another pool is
+    another object), and they must keep their storage.
     """
 
-    __slots__ = ("k", "v", "k_scale", "v_scale", "_bytes")
+    __slots__ = ("_tensors", "_bytes")
 
     def __init__(self, k: torch.Tensor, v: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor):
         for name, t, nd in (("k", k, 4), ("v", v, 4), ("k_scale", k_scale, 2), ("v_scale", v_scale, 2)):
@@ -76,10 +78,15 @@ class PagedCache:
                 raise ValueError(f"cache {name} must have {nd} dims, got {t.dim()}")
             if t.device != k.device:
                 raise ValueError(f"cache tensors on different devices ({k.device} and {t.device})")
-        self.k, self.v, self.k_scale, self.v_scale = k, v, k_scale, v_scale
+        self._tensors = (k, v, k_scale, v_scale)
         self._bytes = b"".join((_PACK4(k.data_ptr(), _dtype(k), 4, *k.shape, *k.stride()),
                                 _PACK4(v.data_ptr(), _dtype(v), 4, *v.shape, *v.stride()),
                                 _desc2("k_scale", k_scale), _desc2("v_scale", v_scale)))
+
+    k = property(lambda self: self._tensors[0])
+    v = property(lambda self: self._tensors[1])
+    k_scale = property(lambda self: self._tensors[2])
+    v_scale = property(lambda self: self._tensors[3])
 
     @property
     def page_tokens(self) -> int:

@@ -7,6 +7,8 @@
 #include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <functional>
+#include <initializer_list>
 
 #include "api_checks.h"
 #include "sdpa_internal.h"
@@ -71,6 +73,17 @@ sdpa_status_t pack_extent(const sdpa_tensor_t* t, const char* name, int64_t rows
     return SDPA_OK;
 }
 
+// Workgroups of a launch, a product of factors >= 0.
+sdpa_status_t grid_ok(std::initializer_list<int64_t> factors) {
+    int64_t n = 1;
+    for (int64_t f : factors)
+        if (__builtin_mul_overflow(n, f, &n) || n > INT32_MAX) return fail(SDPA_ERR_UNSUPPORTED, "grid too large");
+    return SDPA_OK;
+}
+
+// Lengths that the kernels' 32-bit positions, rounded up to tiles and ranges, can hold.
+constexpr int64_t kMaxTokens = int64_t(1) << 30;
+
 // Checks q, k and the sequence bounds; fills what both packed operators share.
 sdpa_status_t pack_args(const sdpa_tensor_t* q, const sdpa_tensor_t* k, int64_t n_seqs, int64_t max_q, int64_t max_k,
                         int enable_gqa, sdpa::PackArgs* a) {
@@ -104,6 +117,8 @@ sdpa_status_t pack_args(const sdpa_tensor_t* q, const sdpa_tensor_t* k, int64_t 
     a->group = a->Hq / a->Hkv;
     a->max_q = (int)std::min<int64_t>(max_q, a->Tq);
     a->max_k = (int)std::min<int64_t>(max_k, a->Tkv);
+    if (a->max_q > kMaxTokens || a->max_k > kMaxTokens)
+        return fail(SDPA_ERR_UNSUPPORTED, "sequences of more than 2^30 tokens are not supported");
     TRY(pack_extent(q, "q", a->max_q, q->sizes[2], &a->q_ext));
     return pack_extent(k, "k", a->max_k, k->sizes[2], &a->k_ext);
 }
@@ -111,11 +126,6 @@ sdpa_status_t pack_args(const sdpa_tensor_t* q, const sdpa_tensor_t* k, int64_t 
 sdpa_status_t check_cu(int64_t n_seqs, const void* cu_q, const void* cu_k, int is_causal) {
     if (n_seqs > 0 && (!cu_q || !cu_k)) return fail(SDPA_ERR_INVALID_ARG, "cu_seqlens_q and cu_seqlens_kv are required");
     if (is_causal < 0 || is_causal > 2) return fail(SDPA_ERR_INVALID_ARG, "is_causal must be 0, 1 or 2");
-    return SDPA_OK;
-}
-
-sdpa_status_t grid_ok(int64_t n) {
-    if (n > INT32_MAX) return fail(SDPA_ERR_UNSUPPORTED, "grid too large");
     return SDPA_OK;
 }
 
@@ -173,8 +183,10 @@ sdpa_status_t cache_args(const sdpa_cache_t* c, int64_t n_seqs, int64_t max_page
         return fail(SDPA_ERR_UNSUPPORTED, "pages of %lld tokens are not implemented (16, 32, 64, 128)", (long long)P);
     if (!head_dim_ok(D)) return fail(SDPA_ERR_UNSUPPORTED, "head dim %lld is not implemented (32, 64, 128)", (long long)D);
     if (n < 1 || H < 1) return fail(SDPA_ERR_INVALID_ARG, "the cache holds no pages or no heads");
-    if (n > INT32_MAX || H > INT32_MAX || n_seqs > INT32_MAX || max_pages * P > INT32_MAX)
+    if (n > INT32_MAX || H > INT32_MAX || n_seqs > INT32_MAX || max_pages > INT32_MAX / P)
         return fail(SDPA_ERR_UNSUPPORTED, "sizes beyond 2^31 are not supported");
+    if (max_pages > kMaxTokens / P)
+        return fail(SDPA_ERR_UNSUPPORTED, "page tables of more than 2^30 tokens are not supported");
     if (n_seqs < 0 || max_pages < 0) return fail(SDPA_ERR_INVALID_ARG, "sequence and page counts must be non-negative");
     if (reinterpret_cast<uintptr_t>(c->k.data) % 16 || reinterpret_cast<uintptr_t>(c->v.data) % 16)
         return fail(SDPA_ERR_UNSUPPORTED, "cache k and v need 16-byte aligned bases");
@@ -224,7 +236,9 @@ sdpa_status_t set_weights(const sdpa_tensor_t* in, sdpa_tensor_t* out, sdpa::Cac
     const int64_t want[3] = {a->B, a->Hkv, in->sizes[2]};
     TRY(check_f32(in, "weights", 3, want));
     TRY(check_f32(out, "weights_out", 3, want));
-    if (in->sizes[2] > INT32_MAX) return fail(SDPA_ERR_UNSUPPORTED, "sizes beyond 2^31 are not supported");
+    if (in->sizes[2] > kMaxTokens) return fail(SDPA_ERR_UNSUPPORTED, "weights of more than 2^30 keys are not supported");
+    if (in->data == out->data && (eff_stride(in, 0) != eff_stride(out, 0) || eff_stride(in, 1) != eff_stride(out, 1)))
+        return fail(SDPA_ERR_INVALID_ARG, "weights and weights_out overlap: one tensor, or two");
     a->w_in = static_cast<const float*>(in->data);
     a->w_out = static_cast<float*>(out->data);
     for (int i = 0; i < 2; ++i) {
@@ -327,7 +341,7 @@ sdpa_status_t sdpa_prompt_fwd(const sdpa_tensor_t* q, const sdpa_tensor_t* k, co
     const int D = (int)q->sizes[2];
     a.groups = prompt_groups(a);
     a.n_blk = (int)cdiv(a.max_q, sdpa::PROMPT_ROWS);
-    TRY(grid_ok(n_seqs * a.Hq * a.n_blk));
+    TRY(grid_ok({n_seqs, a.Hq, a.n_blk}));
     return launched(sdpa::launch_prompt(q->dtype, D, a, hip_stream));
 }
 
@@ -352,6 +366,7 @@ sdpa_status_t sdpa_key_weights(const sdpa_tensor_t* q, const sdpa_tensor_t* k, c
     TRY(pack_args(q, k, n_seqs, max_q, max_k, enable_gqa, &a));
     TRY(check_f32(lse, "lse", 2, q->sizes));
     TRY(check_cu(n_seqs, cu_q, cu_k, is_causal));
+    if (max_k > kMaxTokens) return fail(SDPA_ERR_UNSUPPORTED, "weights of more than 2^30 keys are not supported");
     const int64_t want[3] = {n_seqs, a.Hkv, max_k};
     TRY(check_f32(weights, "weights", 3, want));
     TRY(split_scale(scale, &a.scale_log2, &a.q_mul));
@@ -371,8 +386,8 @@ sdpa_status_t sdpa_key_weights(const sdpa_tensor_t* q, const sdpa_tensor_t* k, c
     a.w_s[0] = eff_stride(weights, 0);
     a.w_s[1] = eff_stride(weights, 1);
     TRY(pack_extent(lse, "lse", a.max_q, 1, &a.l_ext));
-    TRY(grid_ok(n_seqs * a.Hq * a.n_split * a.n_blk));
-    TRY(grid_ok(n_seqs * a.Hkv * 65536));  // rows of the sum's grid
+    TRY(grid_ok({n_seqs, a.Hq, a.n_split, a.n_blk}));
+    TRY(grid_ok({n_seqs, a.Hkv, 65536}));  // rows of the sum's grid
     return launched(sdpa::launch_key_weights(q->dtype, (int)q->sizes[2], a, hip_stream));
 }
 
@@ -401,7 +416,7 @@ sdpa_status_t sdpa_cache_append(const sdpa_cache_t* cache, const sdpa_tensor_t* 
     pack_strides(v, a.nv_s);
     // n tokens that start anywhere touch at most 1 + (n - 1 + P - 1) / P pages
     a.slots = 1 + (a.max_new + a.page - 2) / a.page;
-    TRY(grid_ok(2 * n_seqs * a.Hkv * a.slots));
+    TRY(grid_ok({2, n_seqs, a.Hkv, a.slots}));
     return launched(sdpa::launch_cache_append(k->dtype, a, hip_stream));
 }
 
@@ -453,8 +468,8 @@ sdpa_status_t sdpa_cache_attention(const sdpa_tensor_t* q, const sdpa_cache_t* c
         a.ws_o = reinterpret_cast<float*>(p + w.o);
         if (gather) a.ws_t = reinterpret_cast<float*>(p + w.t);
     }
-    TRY(grid_ok((int64_t)a.row_blocks * a.Hkv * n_seqs * a.n_ranges));
-    TRY(grid_ok(n_seqs * a.Hkv * (a.rows + cdiv(a.w_cols, 256))));
+    TRY(grid_ok({a.row_blocks, a.Hkv, n_seqs, a.n_ranges}));
+    TRY(grid_ok({n_seqs, a.Hkv, a.rows + cdiv(a.w_cols, 256)}));
     return launched(sdpa::launch_cache_attention(q->dtype, a, hip_stream));
 }
 
@@ -469,6 +484,7 @@ sdpa_status_t sdpa_cache_evict(const sdpa_cache_t* cache, const int32_t* page_ta
     TRY(set_table(page_table, table_stride, kv_lens, &a));
     TRY(set_weights(weights, weights_out, &a));
     if (budget < 1 || budget > INT32_MAX) return fail(SDPA_ERR_INVALID_ARG, "budget must be at least 1");
+    if (budget > kMaxTokens) return fail(SDPA_ERR_UNSUPPORTED, "a budget of more than 2^30 tokens is not supported");
     if (recent < 0 || recent > budget) return fail(SDPA_ERR_INVALID_ARG, "recent must lie between 0 and budget");
     const int64_t most = std::min<int64_t>(budget, std::min<int64_t>(max_pages * a.page, a.w_cols));
     if (to_pages < cdiv(most, a.page))
@@ -478,6 +494,8 @@ sdpa_status_t sdpa_cache_evict(const sdpa_cache_t* cache, const int32_t* page_ta
     if (n_seqs == 0) return SDPA_OK;
     if ((!to_table && most > 0) || !kept || !new_lens)
         return fail(SDPA_ERR_INVALID_ARG, "to_table, kept and new_lens are required");
+    if (std::less<const int32_t*>()(new_lens, kv_lens + n_seqs) && std::less<const int32_t*>()(kv_lens, new_lens + n_seqs))
+        return fail(SDPA_ERR_INVALID_ARG, "new_lens overlaps kv_lens");
     a.to = to_table;
     a.to_s = n_seqs > 1 ? to_stride : 0;
     a.to_pages = (int)cdiv(most, a.page);
@@ -485,7 +503,7 @@ sdpa_status_t sdpa_cache_evict(const sdpa_cache_t* cache, const int32_t* page_ta
     a.recent = (int)recent;
     a.kept = kept;
     a.new_lens = new_lens;
-    TRY(grid_ok(2 * n_seqs * a.Hkv * std::max(1, a.to_pages)));
+    TRY(grid_ok({2, n_seqs, a.Hkv, std::max(1, a.to_pages)}));  // the selection is launched without pages too
     return launched(sdpa::launch_cache_evict(a, hip_stream));
 }
 

@@ -85,6 +85,25 @@ def test_prompt_slice_limit():
     assert "1 GiB" in _last()
 
 
+def test_absurd_counts_do_not_wrap():
+    """Counts whose product leaves 64 bits, on tensors of stride 0, are refused rather than launched."""
+    one = torch.empty(64, dtype=torch.float16)
+    big = (1 << 31) - 1
+    lib = S.load_library()
+
+    def t(rows, heads):
+        return V._PACK[3].pack(one.data_ptr(), V._dtype(one), 3, rows, heads, 64, 0, 0, 1)
+    lse = V._PACK[2].pack(one.data_ptr(), 0, 2, 1 << 30, big, 0, 1)
+    q = t(1 << 30, big)
+    assert lib.sdpa_prompt_fwd(q, q, q, CU.data_ptr(), CU.data_ptr(), big, 1 << 30, 1 << 30, 1, 0.1, 0, q, lse,
+                               None) == UNSUPPORTED and "grid" in _last()
+    q, lse = t(big, 1), V._PACK[2].pack(one.data_ptr(), 0, 2, big, 1, 1, 1)
+    assert lib.sdpa_prompt_fwd(q, q, q, CU.data_ptr(), CU.data_ptr(), 2, big, big, 1, 0.1, 0, q, lse,
+                               None) == UNSUPPORTED and "2^30" in _last()
+    n = ctypes.c_size_t(7)
+    assert lib.sdpa_key_weights_workspace_bytes(q, q, 2, 5, big, 0, ctypes.byref(n)) == UNSUPPORTED and n.value == 0
+
+
 def test_prompt_empty_calls_do_nothing():
     assert _prompt(n=0, cu_q=None, cu_k=None) == OK
     assert _prompt(mq=0) == OK
@@ -177,6 +196,8 @@ def test_cache_refusals(change, code, frag):
     (dict(n=-1), INVALID, "non-negative"),
     (dict(pages=-1), INVALID, "non-negative"),
     (dict(pages=1 << 28), UNSUPPORTED, "2^31"),
+    (dict(pages=1 << 62), UNSUPPORTED, "2^31"),
+    (dict(pages=(1 << 26) + 1, stride=1 << 27), UNSUPPORTED, "2^30"),
 ])
 def test_append_refusals(change, code, frag):
     assert _append(**change) == code and frag in _last()
@@ -200,6 +221,7 @@ def _attend(q=None, cache=None, mq=4, mkv=48, causal=1, scale=0.1, gqa=1, w=None
 
 
 W = _z(2, 2, 48, dtype=torch.float32)
+W96 = _z(2, 2, 96, dtype=torch.float32)
 
 
 @pytest.mark.parametrize("change,code,frag", [
@@ -269,6 +291,10 @@ def _evict(cache=None, w=W, wo=W, budget=16, recent=4, to=TABLE, to_pages=1, str
     (dict(w=_z(2, 2, 48)), INVALID, "f32"),
     (dict(w=_z(2, 3, 48, dtype=torch.float32)), INVALID, "weights dim"),
     (dict(wo=None), INVALID, "weights_out"),
+    (dict(budget=(1 << 30) + 1), UNSUPPORTED, "2^30"),
+    (dict(kept=64), INVALID, "new_lens overlaps"),
+    (dict(kept=64, nl=LENS[1:]), INVALID, "new_lens overlaps"),
+    (dict(w=W96[:, :, :48], wo=W96.view(2, 2, 96).as_strided((2, 2, 48), (192, 48, 1)), kept=64), INVALID, "overlap: one"),
 ])
 def test_evict_refusals(change, code, frag):
     assert _evict(**change) == code and frag in _last()
@@ -289,6 +315,8 @@ def test_binding_refusals():
         S.cache_attention(q, c, TABLE, LENS, CU, 4, enable_gqa=True)
     with pytest.raises(ValueError, match="GPU only"):
         S.cache_evict(c, TABLE, LENS, W, 16, 4, TABLE)
+    with pytest.raises(AttributeError):  # the C description of the pool would be another's
+        c.k = c.k.clone()
     with pytest.raises(ValueError, match="dims"):
         S.PagedCache(c.k[0], c.v, c.k_scale, c.v_scale)
     for bad in (CU.long(), CU[None], torch.zeros(6, dtype=torch.int32)[::2]):
