@@ -419,6 +419,7 @@ void sdpa_prompt_kernel(const PackArgs a) {
     auto load_k = [&](int u) SDPA_INLINE { load_tile(kd, lds + (u & 1) * C::TILEB, tile(u), kvo, krow); };
     auto load_v = [&](int u) SDPA_INLINE { load_tile(vd, lds + (2 + (u & 1)) * C::TILEB, tile(u), vvo, vrow); };
 
+    if (tile(0) < ntiles) load_k(0);  // on its way while Q comes
     const int qw = q0 + wave * 32, qi = qw + n;  // this wave's first row; this lane's
     const bool ok = qi < s.nq;
     vec qf[NKS];
@@ -568,7 +569,7 @@ void sdpa_prompt_kernel(const PackArgs a) {
         l = 0.0f;
 #pragma unroll
         for (int d = 0; d < ND; ++d) oacc[d] = f32x16{};
-        if (tile(0) < ntiles) load_k(0);
+        if (again && tile(0) < ntiles) load_k(0);
         int u = 0;
         if (u_end > 0) {
             stage(0);
