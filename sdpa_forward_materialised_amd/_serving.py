@@ -14,6 +14,7 @@ from __future__ import annotations
 
 import ctypes
 import math
+import struct
 from typing import Optional, Tuple
 
 import torch
@@ -35,16 +36,23 @@ def _dtype(t: torch.Tensor) -> int:
     return dt
 
 
+def _refuse_desc(name: str, t: torch.Tensor, n: int):
+    _dtype(t)
+    raise ValueError(f"{name} must have {n} dims, got {t.dim()}") from None
+
+
 def _desc2(name: str, t: torch.Tensor) -> bytes:
-    if t.dim() != 2:
-        raise ValueError(f"{name} must have 2 dims, got {t.dim()}")
-    return _PACK2(t.data_ptr(), _dtype(t), 2, *t.shape, *t.stride())
+    try:
+        return _PACK2(t.data_ptr(), _DTYPES[t.dtype], 2, *t.shape, *t.stride())
+    except (KeyError, struct.error):  # the item count is that of the dims
+        _refuse_desc(name, t, 2)
 
 
 def _desc3(name: str, t: torch.Tensor) -> bytes:
-    if t.dim() != 3:
-        raise ValueError(f"{name} must have 3 dims, got {t.dim()}")
-    return _PACK3(t.data_ptr(), _dtype(t), 3, *t.shape, *t.stride())
+    try:
+        return _PACK3(t.data_ptr(), _DTYPES[t.dtype], 3, *t.shape, *t.stride())
+    except (KeyError, struct.error):
+        _refuse_desc(name, t, 3)
 
 
 def _device(t: torch.Tensor, *others: torch.Tensor) -> int:
@@ -124,10 +132,14 @@ def _table(name: str, t: torch.Tensor, n_seqs: int) -> None:
 
 def _cu_pair(cu_q: torch.Tensor, cu_kv: torch.Tensor) -> int:
     _offsets("cu_seqlens_q", cu_q)
-    _offsets("cu_seqlens_kv", cu_kv)
-    if cu_q.numel() != cu_kv.numel() or cu_q.numel() < 1:
+    n = cu_q.numel()
+    if cu_kv is not cu_q:
+        _offsets("cu_seqlens_kv", cu_kv)
+        if cu_kv.numel() != n:
+            n = 0
+    if n < 1:
         raise ValueError("cu_seqlens_q and cu_seqlens_kv must hold n_seqs + 1 offsets each")
-    return cu_q.numel() - 1
+    return n - 1
 
 
 def _scale(scale: Optional[float], D: int) -> float:
@@ -163,8 +175,7 @@ def _workspace(lib, fn, like: torch.Tensor, sig, *args):
 
 def _outputs(q: torch.Tensor, out) -> Tuple[torch.Tensor, torch.Tensor]:
     if out is None:
-        T, H, D = q.shape
-        return q.new_empty((T, H, D)), q.new_empty((T, H), dtype=torch.float32)
+        return (torch.empty_like(q) if q.is_contiguous() else q.new_empty(q.shape)), q.new_empty(q.shape[:2], dtype=torch.float32)
     O, L = out
     _device(q, O, L)
     return O, L

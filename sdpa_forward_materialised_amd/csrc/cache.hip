@@ -596,10 +596,6 @@ void sdpa_cache_attention_kernel(const CacheArgs a) {
     }
 }
 
-// The ranges joined: O and LSE of every row, and the weights plus each key's
-// sum of probabilities over the rows. Workgroups below n_rows take one row
-// each, the rest 256 keys each of one (sequence, key head). Latency bounds it:
-// a row's statistics are read by all threads at once.
 // reference and sum of a row from its ranges' statistics, read by `n` lanes (a
 // power of two) of which this is `lane`
 __device__ __forceinline__ float2 join_stats(const float2* ml, int nr, int lane, int n) {
@@ -625,6 +621,10 @@ __device__ __forceinline__ float2 join_stats(const float2* ml, int nr, int lane,
     return make_float2(top, sum);
 }
 
+// The ranges joined: O and LSE of every row, and the weights plus each key's
+// sum of probabilities over the rows. Workgroups below n_rows take one row
+// each, the rest 256 keys each of one (sequence, key head). Latency bounds it:
+// a row's statistics are read by all threads at once.
 template <typename T>
 __global__ __attribute__((amdgpu_flat_work_group_size(256, 256)))
 void sdpa_cache_join_kernel(const CacheArgs a, int n_rows) {
