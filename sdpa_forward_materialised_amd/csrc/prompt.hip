@@ -54,8 +54,8 @@ __device__ __forceinline__ void copy_to_lds(desc_t d, uint32_t lds, uint32_t off
 }
 template <int N>
 __device__ __forceinline__ void wait_copies() {
-    static_assert(N < 16, "the low bits of the counter");
-    __builtin_amdgcn_s_waitcnt(0x0F70 | N);
+    static_assert(N < 64, "the counter's six bits");
+    __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | N >> 4 << 14);
 }
 
 // An operand of the products from memory: all loads are in flight before the
@@ -126,9 +126,9 @@ __device__ __forceinline__ uint32_t clean_word(uint32_t w) {
         return lo | hi;
     }
 }
-template <typename T, int BYTES>
+template <typename T, int BYTES, int THREADS = 256>
 __device__ __forceinline__ void clean_tile(uint8_t* tile, int thread) {
-    for (int i = thread; i < BYTES / 16; i += 256) {
+    for (int i = thread; i < BYTES / 16; i += THREADS) {
         u32x4 x = reinterpret_cast<u32x4*>(tile)[i];
 #pragma unroll
         for (int e = 0; e < 4; ++e) x[e] = clean_word<T>(x[e]);
@@ -175,51 +175,61 @@ __device__ __forceinline__ void add_kept(rsrc_t v, uint32_t row_bytes, int j0, i
             }
 }
 
-// O and LSE of the lane's row: x the sum of its half's columns relative to m, l its half of the weights
-template <typename T, int D>
+// O (32-column blocks d0 .. d0 + N - 1 of it) and LSE of the lane's row: x the
+// sum of its half's columns relative to m, l its half of the weights
+template <typename T, int N>
 __device__ __forceinline__ void store_rows(rsrc_t o, rsrc_t lse, const PackArgs& a, int row, bool ok, int hf, const f32x16* x, float m,
-                                           float l) {
+                                           float l, int d0 = 0) {
     const float sum = l + __shfl_xor(l, 32);
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
     const uint32_t ooff = (uint32_t)((ok ? row : 0) * a.o_s[1] * (int)sizeof(T));
 #pragma unroll
-    for (int d = 0; d < D / 32; ++d) {
+    for (int d = 0; d < N; ++d) {
         float y[16];
 #pragma unroll
         for (int r = 0; r < 16; ++r) y[r] = x[d][r] * inv;
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-            if (a.o_vec) store8<T, true>(o, ooff, ok, 32 * d + 16 * c + 8 * hf, D, y + 8 * c);
-            else store8<T, false>(o, ooff, ok, 32 * d + 16 * c + 8 * hf, D, y + 8 * c);
+            const int col = 32 * (d0 + d) + 16 * c + 8 * hf;
+            if (a.o_vec) store8<T, true>(o, ooff, ok, col, col + 8, y + 8 * c);
+            else store8<T, false>(o, ooff, ok, col, col + 8, y + 8 * c);
         }
     }
+    if (d0 > 0) return;
     const float z = sum == 0.0f ? -INFINITY : (m + __builtin_amdgcn_logf(sum)) * LN2;
     __builtin_amdgcn_raw_buffer_store_b32(__builtin_bit_cast(uint32_t, z), lse,
                                           pred(ok && hf == 0, (uint32_t)((ok ? row : 0) * a.l_s[1] * 4)), 0, 0);
 }
 
-// float32: K and V tiles of 32 keys, double-buffered. The matrix instructions
-// (32x32x2, D / 2 of them for the scores and as many for the sums of a tile)
-// bound it. At D = 128 Q and the sums take 128 registers and the operands read
-// ahead the rest: one wave a SIMD, with up to 512 registers (16 heads of 4096
-// tokens, causal: 702 us, 98 TFLOP/s), where two waves of 256 spill (978 us).
-// Below that two waves fit and fill each other's waits (D = 64: 426 us).
+// float32: the matrix instructions (32x32x2, D / 2 of them for the scores and
+// as many for the sums of 32 rows by 32 keys) bound it. A workgroup takes 32
+// rows, and its four waves, one on each SIMD, every fourth key tile each, so
+// that the chain of a call of few rows is a quarter as long as with 32 rows a
+// wave (1024 + 700 tokens, 2 heads of 128: 49 us against 169; 16 heads of 4096
+// tokens: 64 wide 308 against 424, 111 TFLOP/s, 128 wide 689 against 697; only
+// a full chip of short chains loses, 1024 + 1000 tokens, 32 heads of 128: 253
+// against 206). A wave's tiles are its own: it copies them, waits for its own
+// copies (no barrier), and copies the next K behind the score products and the
+// next V behind the sums. At D = 128 Q and the sums take 128 registers and the
+// operands read ahead the rest of 512, so one wave a SIMD; below, two.
 template <int D>
 __global__ __attribute__((amdgpu_flat_work_group_size(256, 256), amdgpu_waves_per_eu(D == 128 ? 1 : 2)))
 void sdpa_prompt_f32_kernel(const PackArgs a) {
-    constexpr int SZ = 4, NW = 4, TN = 32, QB = 32 * NW, ND = D / 32;
+    constexpr int SZ = 4, NW = 4, TN = 32, ND = D / 32;
     using C = TwoPassCfg<float, D, NW, MASK_NONE, true, TN, true>;
     using TR = Tr<float>;
     constexpr int KSTEP = 2 * TR::KH, NKS = D / KSTEP;
-    __shared__ __attribute__((aligned(16))) uint8_t smem[4 * C::TILEB];
+    static_assert(ND * 16 * 64 * 4 <= 2 * C::TILEB, "a wave's sums fit its tiles");
+    __shared__ __attribute__((aligned(16))) uint8_t smem[NW * 2 * C::TILEB];
+    __shared__ float2 ml_s[NW][64];
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 31, hf = lane >> 5;
     const PackWork w = pack_work(blockIdx.x, a.B, a.Hq, a.n_blk);
     const Seq s = sequence(a, w.b);
-    const int q0 = (a.n_blk - 1 - w.blk) * QB;
+    const int q0 = (a.n_blk - 1 - w.blk) * 32;
     if (q0 >= s.nq) return;
-    const int kend = a.causal ? min(s.nk, max(0, min(q0 + QB, s.nq) + s.coff)) : s.nk;
+    const int kend = a.causal ? min(s.nk, max(0, min(q0 + 32, s.nq) + s.coff)) : s.nk;
     const int ntiles = (kend + TN - 1) / TN;
     const int hk = w.h / a.group;
 
@@ -230,120 +240,162 @@ void sdpa_prompt_f32_kernel(const PackArgs a) {
     const rsrc_t lr = make_rsrc(a.lse + s.q0 * a.l_s[1] + w.h * a.l_s[0], a.l_ext);
     const uint32_t krow = (uint32_t)(a.k_s[1] * SZ), vrow = (uint32_t)(a.v_s[1] * SZ);
 
-    const uint32_t lds = lds_address(smem);
-    auto load_tile = [&](int t) SDPA_INLINE {
-        const uint32_t kl = lds + (t & 1) * 2 * C::TILEB, vl = kl + C::TILEB;
+    uint8_t* const kt = smem + wave * 2 * C::TILEB;
+    uint8_t* const vt = kt + C::TILEB;
+    const uint32_t kl = lds_address(kt), vl = kl + C::TILEB;
+    auto load_k = [&](int t) SDPA_INLINE {
 #pragma unroll
-        for (int jj = 0; jj < C::NI / NW; ++jj) {
-            const int j = jj * NW + wave;
+        for (int j = 0; j < C::NI; ++j) {
             const int row = j * C::RPI + lane / C::CPR;
-            const bool ok = t * TN + row < s.nk;
-            const int ck = (lane % C::CPR) ^ C::fk(row), cv = (lane % C::CPR) ^ C::fv(row);
-            copy_to_lds(kd, kl + j * 1024, pred(ok, (uint32_t)(t * TN + row) * krow + ck * 16));
-            copy_to_lds(vd, vl + j * 1024, pred(ok, (uint32_t)(t * TN + row) * vrow + cv * 16));
+            copy_to_lds(kd, kl + j * 1024, pred(t * TN + row < s.nk, (uint32_t)(t * TN + row) * krow +
+                                                                         ((lane % C::CPR) ^ C::fk(row)) * 16));
         }
     };
-    static_assert(C::NI % NW == 0, "tile loads split evenly over the waves");
+    auto load_v = [&](int t) SDPA_INLINE {
+#pragma unroll
+        for (int j = 0; j < C::NI; ++j) {
+            const int row = j * C::RPI + lane / C::CPR;
+            copy_to_lds(vd, vl + j * 1024, pred(t * TN + row < s.nk, (uint32_t)(t * TN + row) * vrow +
+                                                                         ((lane % C::CPR) ^ C::fv(row)) * 16));
+        }
+    };
+    // the wave's LDS reads so far are done, so that a copy may take their place
+    auto reads_done = [&]() SDPA_INLINE {
+        __builtin_amdgcn_sched_barrier(0);
+        __builtin_amdgcn_s_waitcnt(0xC07F);
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    // all but the last N copies have landed
+    auto landed = [&](auto count) SDPA_INLINE {
+        __builtin_amdgcn_sched_barrier(0);
+        wait_copies<decltype(count)::value>();
+        asm volatile("" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+    };
+    constexpr std::integral_constant<int, C::NI> one_tile{};
+    constexpr std::integral_constant<int, 0> none{};
 
-    const int qw = q0 + wave * 32, qi = qw + n;  // this wave's first row; this lane's
-    float qf[NKS];
+    const int qi = q0 + n;  // this lane's row
     const bool ok = qi < s.nq;
     const uint32_t qoff = (uint32_t)((ok ? qi : 0) * a.q_s[1] * SZ);
+    float qf[NKS];
     uint32_t qo[NKS];
 #pragma unroll
     for (int c = 0; c < NKS; ++c) qo[c] = pred(ok, qoff + (c * KSTEP + hf * TR::KH) * SZ);
     load_operands<float, NKS>(qr, qo, a.q_mul, qf);
+    // the first tile with a key that some row does not keep
+    const int t_cut = (a.causal ? max(0, min(s.nk, q0 + s.coff + 1)) : s.nk) / TN;
+    const int kr0 = swap23(n);
     f32x16 oacc[ND];
     float m, l;
-    const int kr0 = swap23(n);
-
-    auto tile = [&](int t, bool edge) SDPA_INLINE {
-        const uint8_t* const kt = smem + (t & 1) * 2 * C::TILEB;
-        const uint8_t* const vt = kt + C::TILEB;
-        f32x16 acc = {};
-#pragma unroll
-        for (int c = 0; c < NKS; ++c) {
-            const int elem = c * KSTEP + hf * TR::KH;
-            const float ka = *reinterpret_cast<const float*>(kt + C::pos_k(kr0, elem * SZ / 16) * 16 + ((elem * SZ) & 15));
-            acc = TR::mfma(ka, qf[c], acc);
-        }
-        if (edge) {
-            const int lim = min(s.nk - 1 - t * TN, a.causal ? qi + s.coff - t * TN : 0x7fffffff) - 8 * hf;
-#pragma unroll
-            for (int r = 0; r < 16; ++r) acc[r] = kk(0, r) > lim ? -INFINITY : acc[r];
-        }
-        float top = acc[0];
-#pragma unroll
-        for (int r = 1; r < 16; ++r) top = fmaxf(top, acc[r]);
-        top *= a.scale_log2;
-        if (__builtin_amdgcn_ballot_w64(top > m + 8.0f) != 0) {
-            const float up = fmaxf(m, fmaxf(top, __shfl_xor(top, 32)));
-            const float f = up == -INFINITY ? 1.0f : fast_exp2(m - up);
-            m = up;
-            l *= f;
-#pragma unroll
-            for (int d = 0; d < ND; ++d)
-#pragma unroll
-                for (int r = 0; r < 16; ++r) oacc[d][r] *= f;
-        }
-        float p[16];
-        const float mu = m == -INFINITY ? 0.0f : m;
-        float sum = 0.0f;
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-            p[r] = fast_exp2(__builtin_fmaf(acc[r], a.scale_log2, -mu));
-            sum += p[r];
-        }
-        l += sum;
-        // A^T += V^T P^T
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-            const int row = kk(hf, r);
-#pragma unroll
-            for (int d = 0; d < ND; ++d) {
-                const int col = 32 * d + swap23(n);
-                const float va = *reinterpret_cast<const float*>(vt + C::pos_v(row, col * SZ / 16) * 16 + ((col * SZ) & 15));
-                oacc[d] = TR::mfma(va, p[r], oacc[d]);
-            }
-        }
-    };
-
-    // tiles before t_full hold kept keys only, for every row of the wave;
-    // tiles from t_end on none
-    const int last_row = min(qw + 32, s.nq) - 1;
-    const bool live = qw < s.nq;
-    const int t_end = !live ? 0 : a.causal ? max(0, min(ntiles, (last_row + s.coff + TN) / TN)) : ntiles;
-    const int t_full = min(t_end, (a.causal ? max(0, min(s.nk, qw + s.coff + 1)) : s.nk) / TN);
-    // the first tile with a key that some row of the workgroup does not keep
-    const int t_cut = (a.causal ? max(0, min(s.nk, q0 + s.coff + 1)) : s.nk) / TN;
     bool again = false;
     for (;;) {
         m = -INFINITY;
         l = 0.0f;
 #pragma unroll
         for (int d = 0; d < ND; ++d) oacc[d] = f32x16{};
-        if (ntiles > 0) load_tile(0);
-        wait_copies<0>();
-        __syncthreads();
-        for (int t = 0; t < ntiles; ++t) {
-            if (again && t >= t_cut) {
-                clean_tile<float, C::TILEB>(smem + ((t & 1) * 2 + 1) * C::TILEB, threadIdx.x);
-                __syncthreads();
-            }
-            if (t + 1 < ntiles) load_tile(t + 1);
-            if (t < t_end) tile(t, t >= t_full);
-            wait_copies<0>();
-            __syncthreads();
+        if (wave < ntiles) {
+            load_k(wave);
+            load_v(wave);
         }
-        if (again || t_cut >= ntiles) break;
-        again = __syncthreads_or(!all_finite<ND>(oacc)) != 0;
-        if (!again) break;
+        for (int t = wave; t < ntiles; t += NW) {
+            const bool more = t + NW < ntiles;
+            landed(one_tile);
+            f32x16 acc = {};
+#pragma unroll
+            for (int c = 0; c < NKS; ++c) {
+                const int elem = c * KSTEP + hf * TR::KH;
+                const float ka = *reinterpret_cast<const float*>(kt + C::pos_k(kr0, elem * SZ / 16) * 16 + ((elem * SZ) & 15));
+                acc = TR::mfma(ka, qf[c], acc);
+            }
+            reads_done();
+            if (more) load_k(t + NW);
+            if (t >= t_cut) {
+                const int lim = min(s.nk - 1 - t * TN, a.causal ? qi + s.coff - t * TN : 0x7fffffff) - 8 * hf;
+#pragma unroll
+                for (int r = 0; r < 16; ++r) acc[r] = kk(0, r) > lim ? -INFINITY : acc[r];
+            }
+            float top = acc[0];
+#pragma unroll
+            for (int r = 1; r < 16; ++r) top = fmaxf(top, acc[r]);
+            top *= a.scale_log2;
+            if (__builtin_amdgcn_ballot_w64(top > m + 8.0f) != 0) {
+                const float up = fmaxf(m, fmaxf(top, __shfl_xor(top, 32)));
+                const float f = up == -INFINITY ? 1.0f : fast_exp2(m - up);
+                m = up;
+                l *= f;
+#pragma unroll
+                for (int d = 0; d < ND; ++d)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) oacc[d][r] *= f;
+            }
+            float p[16];
+            const float mu = m == -INFINITY ? 0.0f : m;
+            float sum = 0.0f;
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                p[r] = fast_exp2(__builtin_fmaf(acc[r], a.scale_log2, -mu));
+                sum += p[r];
+            }
+            l += sum;
+            if (more) landed(one_tile);
+            else landed(none);
+            if (again && t >= t_cut) {
+                clean_tile<float, C::TILEB, 64>(vt, lane);
+                reads_done();
+            }
+            // A^T += V^T P^T
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                const int row = kk(hf, r);
+#pragma unroll
+                for (int d = 0; d < ND; ++d) {
+                    const int col = 32 * d + swap23(n);
+                    const float va = *reinterpret_cast<const float*>(vt + C::pos_v(row, col * SZ / 16) * 16 + ((col * SZ) & 15));
+                    oacc[d] = TR::mfma(va, p[r], oacc[d]);
+                }
+            }
+            reads_done();
+            if (more) load_v(t + NW);
+        }
+        // a wave's tiles are its own, and so is taking them again
+        if (again || t_cut >= ntiles || __builtin_amdgcn_ballot_w64(!all_finite<ND>(oacc)) == 0) break;
+        again = true;
     }
     if (again) {
         const rsrc_t vr = make_rsrc(static_cast<const float*>(a.v) + s.k0 * a.v_s[1] + hk * a.v_s[0], a.v_ext);
-        add_kept<float, ND>(vr, vrow, t_cut * TN, kend, a.causal ? qi + s.coff : s.nk - 1, hf, oacc);
+        for (int t = wave; t < ntiles; t += NW)
+            if (t >= t_cut)
+                add_kept<float, ND>(vr, vrow, t * TN, min(kend, t * TN + TN), a.causal ? qi + s.coff : s.nk - 1, hf, oacc);
     }
-    store_rows<float, D>(orr, lr, a, qi, ok, hf, oacc, m, l);
+
+    // the waves' sums joined, 32 columns a wave
+    float* const js = reinterpret_cast<float*>(smem) + lane;
+    constexpr int WS = 2 * C::TILEB / 4;
+    ml_s[wave][lane] = make_float2(m, l);
+#pragma unroll
+    for (int d = 0; d < ND; ++d)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) js[wave * WS + (d * 16 + r) * 64] = oacc[d][r];
+    __syncthreads();
+    if (wave >= ND) return;
+    float2 o[NW];
+    m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < NW; ++i) {
+        o[i] = ml_s[i][lane];
+        m = fmaxf(m, o[i].x);
+    }
+    l = 0.0f;
+    f32x16 x = {};
+#pragma unroll
+    for (int i = 0; i < NW; ++i) {
+        const float f = o[i].x == -INFINITY ? 0.0f : fast_exp2(o[i].x - m);
+        l += o[i].y * f;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) x[r] += js[i * WS + (wave * 16 + r) * 64] * f;
+    }
+    store_rows<float, 1>(orr, lr, a, qi, ok, hf, &x, m, l, wave);
 }
 
 // The same for 16-bit types, with the three parts of neighbouring 32-key
@@ -618,15 +670,15 @@ void sdpa_prompt_kernel(const PackArgs a) {
         const rsrc_t vr = make_rsrc(static_cast<const T*>(a.v) + s.k0 * a.v_s[1] + hk * a.v_s[0], a.v_ext);
         add_kept<T, ND>(vr, vrow, t_cut * TN, kend, a.causal ? qi + s.coff : s.nk - 1, hf, oacc);
     }
-    store_rows<T, D>(orr, lr, a, qi, ok, hf, oacc, m, l);
+    store_rows<T, ND>(orr, lr, a, qi, ok, hf, oacc, m, l);
 }
 
 template <typename T, int NG>
 static int launch_prompt_t(int D, const PackArgs& a, hipStream_t s) {
     const dim3 grid((uint32_t)a.B * a.Hq * a.n_blk), block(256 * NG);
-#define SDPA_PROMPT(D)                                                                   \
-    if constexpr (sizeof(T) == 4) sdpa_prompt_f32_kernel<D><<<grid, block, 0, s>>>(a);   \
-    else sdpa_prompt_kernel<T, D, NG><<<grid, block, 0, s>>>(a);
+#define SDPA_PROMPT(D)                                                                    \
+    if constexpr (sizeof(T) == 2) sdpa_prompt_kernel<T, D, NG><<<grid, block, 0, s>>>(a); \
+    else sdpa_prompt_f32_kernel<D><<<grid, block, 0, s>>>(a);
     switch (D) {
         case 32: SDPA_PROMPT(32) break;
         case 64: SDPA_PROMPT(64) break;

@@ -37,7 +37,8 @@ struct PackArgs {
     uint32_t q_ext, k_ext, v_ext, o_ext, l_ext;  // byte extents of one (sequence, head) slice
 };
 
-constexpr int PROMPT_ROWS = 128;  // query rows of one workgroup of the prompt kernels
+constexpr int PROMPT_ROWS = 128;     // query rows of one workgroup of the 16-bit prompt kernel
+constexpr int PROMPT_ROWS_F32 = 32;  // and of the float32 kernel
 int launch_prompt(int dtype, int D, const PackArgs& a, void* stream);
 constexpr int KEY_WEIGHT_KEYS = 128;  // keys of one workgroup of the key-weight kernel
 int launch_key_weights(int dtype, int D, const PackArgs& a, void* stream);

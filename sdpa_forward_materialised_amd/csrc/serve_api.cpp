@@ -129,7 +129,7 @@ sdpa_status_t check_cu(int64_t n_seqs, const void* cu_q, const void* cu_k, int i
     return SDPA_OK;
 }
 
-// Prompt attention: two groups of four waves a workgroup, each on every other
+// Prompt attention, 16-bit types: two groups of four waves a workgroup, each on every other
 // key tile, where one group a block leaves wave slots empty (512 workgroups of
 // four waves fill two slots of every SIMD) and the chain of tiles is long
 // enough to pay for joining the groups. Measured, one group and two: 4096
@@ -340,7 +340,7 @@ sdpa_status_t sdpa_prompt_fwd(const sdpa_tensor_t* q, const sdpa_tensor_t* k, co
     TRY(pack_extent(lse, "lse", a.max_q, 1, &a.l_ext));
     const int D = (int)q->sizes[2];
     a.groups = prompt_groups(a);
-    a.n_blk = (int)cdiv(a.max_q, sdpa::PROMPT_ROWS);
+    a.n_blk = (int)cdiv(a.max_q, q->dtype == SDPA_F32 ? sdpa::PROMPT_ROWS_F32 : sdpa::PROMPT_ROWS);
     TRY(grid_ok({n_seqs, a.Hq, a.n_blk}));
     return launched(sdpa::launch_prompt(q->dtype, D, a, hip_stream));
 }

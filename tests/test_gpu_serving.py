@@ -61,6 +61,12 @@ PROMPTS = [
     ("long-bf16-d32-gqa7", 5, [700], [700], 7, 1, 32, "bf16", True, "top_left", None),
     ("f32-d128", 6, [65, 100], [65, 100], 2, 1, 128, "f32", True, "top_left", None),
     ("f32-d64-odd", 7, [33, 1, 190], [33, 1, 190], 3, 3, 64, "f32", True, "top_left", None),
+    ("f32-long", 21, [700, 3], [700, 3], 2, 2, 64, "f32", True, "top_left", None),
+    ("f32-d128-bottom-right", 22, [70, 500], [300, 530], 2, 1, 128, "f32", True, "bottom_right", None),
+    ("f32-d32-noncausal", 23, [40, 90], [333, 20], 4, 2, 32, "f32", False, "top_left", None),
+    ("f16-d64-blocks", 24, [1, 31, 33, 97, 800], [1, 31, 33, 97, 800], 2, 1, 64, "f16", True, "top_left", None),
+    ("bf16-d32-bottom-right", 25, [5, 300, 64], [900, 300, 777], 4, 2, 32, "bf16", True, "bottom_right", None),
+    ("f16-d128-noncausal", 26, [33, 129], [800, 95], 2, 1, 128, "f16", False, "top_left", None),
     ("chunk-bottom-right", 8, [16, 100, 37], [200, 100, 300], 4, 2, 64, "f16", True, "bottom_right", None),
     ("more-queries-than-keys", 9, [90, 40], [30, 0], 2, 2, 128, "bf16", True, "bottom_right", None),
     ("noncausal", 10, [5, 9, 64], [77, 0, 129], 2, 2, 128, "bf16", False, "top_left", None),
@@ -98,7 +104,7 @@ def test_prompt_and_weights(case):
 
 
 @pytest.mark.parametrize("dt,D,n", [("bf16", 128, 300), ("f16", 64, 130), ("f32", 32, 100), ("bf16", 32, 900),
-                                    ("f16", 128, 1000), ("f32", 128, 70)])
+                                    ("f16", 128, 1000), ("f32", 128, 70), ("f32", 64, 600), ("f16", 64, 1100)])
 def test_prompt_values_that_are_not_finite(dt, D, n):
     """NaN and infinities in keys and values reach the rows that keep them, and no other."""
     S = _lib()
