@@ -58,6 +58,22 @@ __device__ __forceinline__ void wait_copies() {
     __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | N >> 4 << 14);
 }
 
+// For a wave that copies its own tiles, without barriers: all but the last N
+// copies have landed; its LDS reads are done, so that a copy may take their
+// place. Neither reads nor products move across.
+template <int N>
+__device__ __forceinline__ void landed() {
+    __builtin_amdgcn_sched_barrier(0);
+    wait_copies<N>();
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+}
+__device__ __forceinline__ void reads_done() {
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_waitcnt(0xC07F);
+    __builtin_amdgcn_sched_barrier(0);
+}
+
 // An operand of the products from memory: all loads are in flight before the
 // first is touched.
 template <typename T, int N>
@@ -201,6 +217,39 @@ __device__ __forceinline__ void store_rows(rsrc_t o, rsrc_t lse, const PackArgs&
                                           pred(ok && hf == 0, (uint32_t)((ok ? row : 0) * a.l_s[1] * 4)), 0, 0);
 }
 
+// The sums of four waves that took every fourth key block of the same rows,
+// joined and stored, 32 columns a wave. x: `pitch` floats of LDS for each wave,
+// its own until here.
+template <typename T, int ND>
+__device__ __forceinline__ void join_waves(rsrc_t o, rsrc_t lse, const PackArgs& a, int row, bool ok, int hf, int lane, int wave,
+                                           const f32x16* sums, float m, float l, float* x, int pitch, float2 (*ml)[64]) {
+    constexpr int NW = 4;
+    float* const js = x + lane;
+    ml[wave][lane] = make_float2(m, l);
+#pragma unroll
+    for (int d = 0; d < ND; ++d)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) js[wave * pitch + (d * 16 + r) * 64] = sums[d][r];
+    __syncthreads();
+    if (wave >= ND) return;
+    float2 e[NW];
+    float up = -INFINITY, total = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NW; ++i) {
+        e[i] = ml[i][lane];
+        up = fmaxf(up, e[i].x);
+    }
+    f32x16 y = {};
+#pragma unroll
+    for (int i = 0; i < NW; ++i) {
+        const float f = e[i].x == -INFINITY ? 0.0f : fast_exp2(e[i].x - up);
+        total += e[i].y * f;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) y[r] += js[i * pitch + (wave * 16 + r) * 64] * f;
+    }
+    store_rows<T, 1>(o, lse, a, row, ok, hf, &y, up, total, wave);
+}
+
 // float32: the matrix instructions (32x32x2, D / 2 of them for the scores and
 // as many for the sums of 32 rows by 32 keys) bound it. A workgroup takes 32
 // rows, and its four waves, one on each SIMD, every fourth key tile each, so
@@ -259,21 +308,6 @@ void sdpa_prompt_f32_kernel(const PackArgs a) {
                                                                          ((lane % C::CPR) ^ C::fv(row)) * 16));
         }
     };
-    // the wave's LDS reads so far are done, so that a copy may take their place
-    auto reads_done = [&]() SDPA_INLINE {
-        __builtin_amdgcn_sched_barrier(0);
-        __builtin_amdgcn_s_waitcnt(0xC07F);
-        __builtin_amdgcn_sched_barrier(0);
-    };
-    // all but the last N copies have landed
-    auto landed = [&](auto count) SDPA_INLINE {
-        __builtin_amdgcn_sched_barrier(0);
-        wait_copies<decltype(count)::value>();
-        asm volatile("" ::: "memory");
-        __builtin_amdgcn_sched_barrier(0);
-    };
-    constexpr std::integral_constant<int, C::NI> one_tile{};
-    constexpr std::integral_constant<int, 0> none{};
 
     const int qi = q0 + n;  // this lane's row
     const bool ok = qi < s.nq;
@@ -300,7 +334,7 @@ void sdpa_prompt_f32_kernel(const PackArgs a) {
         }
         for (int t = wave; t < ntiles; t += NW) {
             const bool more = t + NW < ntiles;
-            landed(one_tile);
+            landed<C::NI>();
             f32x16 acc = {};
 #pragma unroll
             for (int c = 0; c < NKS; ++c) {
@@ -338,8 +372,8 @@ void sdpa_prompt_f32_kernel(const PackArgs a) {
                 sum += p[r];
             }
             l += sum;
-            if (more) landed(one_tile);
-            else landed(none);
+            if (more) landed<C::NI>();
+            else landed<0>();
             if (again && t >= t_cut) {
                 clean_tile<float, C::TILEB, 64>(vt, lane);
                 reads_done();
@@ -369,33 +403,7 @@ void sdpa_prompt_f32_kernel(const PackArgs a) {
                 add_kept<float, ND>(vr, vrow, t * TN, min(kend, t * TN + TN), a.causal ? qi + s.coff : s.nk - 1, hf, oacc);
     }
 
-    // the waves' sums joined, 32 columns a wave
-    float* const js = reinterpret_cast<float*>(smem) + lane;
-    constexpr int WS = 2 * C::TILEB / 4;
-    ml_s[wave][lane] = make_float2(m, l);
-#pragma unroll
-    for (int d = 0; d < ND; ++d)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) js[wave * WS + (d * 16 + r) * 64] = oacc[d][r];
-    __syncthreads();
-    if (wave >= ND) return;
-    float2 o[NW];
-    m = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < NW; ++i) {
-        o[i] = ml_s[i][lane];
-        m = fmaxf(m, o[i].x);
-    }
-    l = 0.0f;
-    f32x16 x = {};
-#pragma unroll
-    for (int i = 0; i < NW; ++i) {
-        const float f = o[i].x == -INFINITY ? 0.0f : fast_exp2(o[i].x - m);
-        l += o[i].y * f;
-#pragma unroll
-        for (int r = 0; r < 16; ++r) x[r] += js[i * WS + (wave * 16 + r) * 64] * f;
-    }
-    store_rows<float, 1>(orr, lr, a, qi, ok, hf, &x, m, l, wave);
+    join_waves<float, ND>(orr, lr, a, qi, ok, hf, lane, wave, oacc, m, l, reinterpret_cast<float*>(smem), 2 * C::TILEB / 4, ml_s);
 }
 
 // The same for 16-bit types, with the three parts of neighbouring 32-key
@@ -407,21 +415,27 @@ void sdpa_prompt_f32_kernel(const PackArgs a) {
 // reference rises to the row's maximum, A and l are scaled and the block's
 // weights taken again, while its scores are still there.
 //
-// NG: groups of four waves. With two, they take the same rows and every other
-// tile each, and join their sums at the end: for calls whose blocks leave the
-// chip's wave slots empty, the chain of tiles is half as long.
+// NG: key groups, for calls whose blocks of 128 rows leave the chip's wave
+// slots empty. With two, a workgroup is twice four waves, which take the same
+// rows and every other tile each and join their sums at the end: the chain of
+// tiles is half as long. With four (D of 32 and 64, whose tiles fit two
+// workgroups a CU that way) it is 32 rows and four waves that take every fourth
+// block of 32 keys each, from tiles of their own and so without barriers, as
+// the float32 kernel.
 template <typename T, int D, int NG>
 struct PromptCfg {
     static constexpr int NW = 4, TN = 64;
     using C = TwoPassCfg<T, D, NW, MASK_NONE, true, TN, true>;
-    static constexpr int QB = 32 * NW;
+    static constexpr int QB = NG == 4 ? 32 : 32 * NW;
+    static constexpr int THREADS = NG == 2 ? 512 : 256;
+    // two K and two V tiles for a group of four waves, one of each for a wave of its own
+    static constexpr int TILE_BYTES = (NG == 4 ? 2 : 4) * NG * C::TILEB;
     static constexpr int JOIN_BYTES = NG > 1 ? NW * (D / 32) * 16 * 64 * 4 : 0;  // one group's sums
-    static constexpr int TILE_BYTES = NG * 4 * C::TILEB;
     static constexpr int LDS_BYTES = TILE_BYTES > JOIN_BYTES ? TILE_BYTES : JOIN_BYTES;
 };
 
 template <typename T, int D, int NG>
-__global__ __attribute__((amdgpu_flat_work_group_size(256 * NG, 256 * NG), amdgpu_waves_per_eu(2)))
+__global__ __attribute__((amdgpu_flat_work_group_size(PromptCfg<T, D, NG>::THREADS, PromptCfg<T, D, NG>::THREADS), amdgpu_waves_per_eu(2)))
 void sdpa_prompt_kernel(const PackArgs a) {
     using P = PromptCfg<T, D, NG>;
     using C = typename P::C;
@@ -430,18 +444,15 @@ void sdpa_prompt_kernel(const PackArgs a) {
     constexpr int SZ = 2, NW = P::NW, TN = P::TN, ND = D / 32, NKS = D / 16;
     constexpr int EPS = 16 / NKS;  // exponentials beside each of a step's products
     __shared__ __attribute__((aligned(16))) uint8_t smem[P::LDS_BYTES];
-    __shared__ float2 ml_s[NG > 1 ? NW * 64 : 1];
+    __shared__ float2 ml_s[NG > 1 ? NW : 1][64];
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) % NW;
-    const int grp = NG > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 8) : 0;
-    uint8_t* const buf = smem + grp * 4 * C::TILEB;  // this group's tiles
     const int n = lane & 31, hf = lane >> 5;
     const PackWork w = pack_work(blockIdx.x, a.B, a.Hq, a.n_blk);
     const Seq s = sequence(a, w.b);
     const int q0 = (a.n_blk - 1 - w.blk) * P::QB;
     if (q0 >= s.nq) return;
     const int kend = a.causal ? min(s.nk, max(0, min(q0 + P::QB, s.nq) + s.coff)) : s.nk;
-    const int ntiles = (kend + TN - 1) / TN;
     const int hk = w.h / a.group;
 
     const rsrc_t qr = make_rsrc(static_cast<const T*>(a.q) + s.q0 * a.q_s[1] + w.h * a.q_s[0], a.q_ext);
@@ -451,28 +462,7 @@ void sdpa_prompt_kernel(const PackArgs a) {
     const rsrc_t lr = make_rsrc(a.lse + s.q0 * a.l_s[1] + w.h * a.l_s[0], a.l_ext);
     const uint32_t krow = (uint32_t)(a.k_s[1] * SZ), vrow = (uint32_t)(a.v_s[1] * SZ);
 
-    // K tiles in buffers 0 and 1, V tiles in 2 and 3. A wave's loads of a tile
-    // lie NW * RPI rows apart, where the layouts' chunk order repeats: one
-    // lane offset each for K and V, the rest is uniform.
-    constexpr int LROWS = NW * C::RPI;
-    static_assert(C::fk(LROWS) == 0 && C::fv(LROWS) == 0, "the chunk order repeats from one load to the next");
-    const int lrow = wave * C::RPI + lane / C::CPR;
-    const uint32_t kvo = lrow * krow + ((lane % C::CPR) ^ C::fk(lrow)) * 16;
-    const uint32_t vvo = lrow * vrow + ((lane % C::CPR) ^ C::fv(lrow)) * 16;
-    auto load_tile = [&](desc_t r, uint32_t dst, int t, uint32_t vo, uint32_t row) SDPA_INLINE {
-        const int limit = s.nk - t * TN;
-#pragma unroll
-        for (int jj = 0; jj < C::NI / NW; ++jj)
-            copy_to_lds(r, dst + (jj * NW + wave) * 1024,
-                        pred(lrow + jj * LROWS < limit, vo + (uint32_t)(t * TN + jj * LROWS) * row));
-    };
-    const uint32_t lds = lds_address(buf);
-    auto tile = [&](int u) SDPA_INLINE { return u * NG + grp; };  // this group's tile u
-    auto load_k = [&](int u) SDPA_INLINE { load_tile(kd, lds + (u & 1) * C::TILEB, tile(u), kvo, krow); };
-    auto load_v = [&](int u) SDPA_INLINE { load_tile(vd, lds + (2 + (u & 1)) * C::TILEB, tile(u), vvo, vrow); };
-
-    if (tile(0) < ntiles) load_k(0);  // on its way while Q comes
-    const int qw = q0 + wave * 32, qi = qw + n;  // this wave's first row; this lane's
+    const int qw = NG == 4 ? q0 : q0 + wave * 32, qi = qw + n;  // this wave's first row; this lane's
     const bool ok = qi < s.nq;
     vec qf[NKS];
     const uint32_t qoff = (uint32_t)((ok ? qi : 0) * a.q_s[1] * SZ);
@@ -586,114 +576,232 @@ void sdpa_prompt_kernel(const PackArgs a) {
     };
     static_assert(2 * ND == NKS, "as many V as K operands in a step");
 
-    // tiles before t_full hold kept keys only, for every row of the wave;
-    // tiles from t_end on none
-    const int last_row = min(qw + 32, s.nq) - 1;
-    const bool live = qw < s.nq;
-    const int t_end = !live ? 0 : a.causal ? max(0, min(ntiles, (last_row + s.coff + TN) / TN)) : ntiles;
-    const int t_full = min(t_end, (a.causal ? max(0, min(s.nk, qw + s.coff + 1)) : s.nk) / TN);
     constexpr std::integral_constant<int, 0> even{};
     constexpr std::integral_constant<int, 1> odd{};
     constexpr std::true_type on{};
     constexpr std::false_type off{};
-    // the first tile with a key that some row of the workgroup does not keep
-    const int t_cut = (a.causal ? max(0, min(s.nk, q0 + s.coff + 1)) : s.nk) / TN;
-    bool again = false;
-    // iteration u of the group's tiles: K tile u and V tile u - 1 are staged;
-    // the second half of tile u - 1 and the first of tile u are taken
-    auto stage = [&](int u) SDPA_INLINE {
-        wait_copies<0>();
-        __syncthreads();
-        if (again) {  // V tile u - 1, wherever some row of the workgroup does not keep all of it
-            if (u > 0 && tile(u - 1) >= t_cut && tile(u - 1) < ntiles)
-                clean_tile<T, C::TILEB>(buf + (2 + ((u - 1) & 1)) * C::TILEB, threadIdx.x & 255);
-            __syncthreads();
-        }
-        if (tile(u + 1) < ntiles) load_k(u + 1);
-        if (tile(u) < ntiles) load_v(u);
-    };
-    auto kt = [&](int u) SDPA_INLINE -> const uint8_t* { return buf + (u & 1) * C::TILEB; };
-    auto vt = [&](int u) SDPA_INLINE -> const uint8_t* { return buf + (2 + ((u - 1) & 1)) * C::TILEB; };
-    const int u_all = (ntiles + NG - 1) / NG;  // iterations of the longest group
-    const int u_end = NG == 1 ? t_end : t_end > grp ? (t_end - grp + NG - 1) / NG : 0;  // this wave's tiles
-    for (;;) {
+    auto start = [&]() SDPA_INLINE {
         m = -INFINITY;
         l = 0.0f;
 #pragma unroll
         for (int d = 0; d < ND; ++d) oacc[d] = f32x16{};
-        if (again && tile(0) < ntiles) load_k(0);
-        int u = 0;
-        if (u_end > 0) {
-            stage(0);
-            step(odd, off, on, off, false, -1, kt(0), vt(0));
-            step(even, on, on, off, tile(0) >= t_full, 2 * tile(0), kt(0), vt(0));
-            for (u = 1; u < u_end; ++u) {
-                stage(u);
-                step(odd, on, on, on, tile(u - 1) >= t_full, 2 * tile(u - 1) + 1, kt(u), vt(u));
-                step(even, on, on, on, tile(u) >= t_full, 2 * tile(u), kt(u), vt(u));
-            }
-            stage(u);
-            step(odd, on, off, on, tile(u - 1) >= t_full, 2 * tile(u - 1) + 1, kt(u), vt(u));
-            step(even, off, off, on, false, 0, kt(u), vt(u));
-            ++u;
-        }
-        for (; u <= u_all; ++u) stage(u);
-        if (again || t_cut >= ntiles) break;
-        again = __syncthreads_or(!all_finite<ND>(oacc)) != 0;
-        if (!again) break;
-    }
+    };
+    // the first key that some row of the workgroup does not keep
+    const int first_cut = a.causal ? max(0, min(s.nk, q0 + s.coff + 1)) : s.nk;
+    bool again = false;
 
-    if constexpr (NG > 1) {  // the second group's sums, then the first's join them
-        float* const js = reinterpret_cast<float*>(smem) + wave * ND * 16 * 64 + lane;
-        __syncthreads();
-        if (grp == 1) {
-            ml_s[wave * 64 + lane] = make_float2(m, l);
+    if constexpr (NG < 4) {
+        const int grp = NG > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x >> 8) : 0;
+        uint8_t* const buf = smem + grp * 4 * C::TILEB;  // this group's tiles
+        // K tiles in buffers 0 and 1, V tiles in 2 and 3. A wave's loads of a
+        // tile lie NW * RPI rows apart, where the layouts' chunk order repeats:
+        // one lane offset each for K and V, the rest is uniform.
+        constexpr int LROWS = NW * C::RPI;
+        static_assert(C::fk(LROWS) == 0 && C::fv(LROWS) == 0, "the chunk order repeats from one load to the next");
+        const int lrow = wave * C::RPI + lane / C::CPR;
+        const uint32_t kvo = lrow * krow + ((lane % C::CPR) ^ C::fk(lrow)) * 16;
+        const uint32_t vvo = lrow * vrow + ((lane % C::CPR) ^ C::fv(lrow)) * 16;
+        auto load_tile = [&](desc_t r, uint32_t dst, int t, uint32_t vo, uint32_t row) SDPA_INLINE {
+            const int limit = s.nk - t * TN;
+#pragma unroll
+            for (int jj = 0; jj < C::NI / NW; ++jj)
+                copy_to_lds(r, dst + (jj * NW + wave) * 1024,
+                            pred(lrow + jj * LROWS < limit, vo + (uint32_t)(t * TN + jj * LROWS) * row));
+        };
+        const uint32_t lds = lds_address(buf);
+        auto tile = [&](int u) SDPA_INLINE { return u * NG + grp; };  // this group's tile u
+        auto load_k = [&](int u) SDPA_INLINE { load_tile(kd, lds + (u & 1) * C::TILEB, tile(u), kvo, krow); };
+        auto load_v = [&](int u) SDPA_INLINE { load_tile(vd, lds + (2 + (u & 1)) * C::TILEB, tile(u), vvo, vrow); };
+        // tiles before t_full hold kept keys only, for every row of the wave;
+        // tiles from t_end on none
+        const int ntiles = (kend + TN - 1) / TN;
+        const int last_row = min(qw + 32, s.nq) - 1;
+        const bool live = qw < s.nq;
+        const int t_end = !live ? 0 : a.causal ? max(0, min(ntiles, (last_row + s.coff + TN) / TN)) : ntiles;
+        const int t_full = min(t_end, (a.causal ? max(0, min(s.nk, qw + s.coff + 1)) : s.nk) / TN);
+        const int t_cut = first_cut / TN;
+        // iteration u of the group's tiles: K tile u and V tile u - 1 are
+        // staged; the second half of tile u - 1 and the first of tile u are taken
+        auto stage = [&](int u) SDPA_INLINE {
+            wait_copies<0>();
+            __syncthreads();
+            if (again) {  // V tile u - 1, wherever some row of the workgroup does not keep all of it
+                if (u > 0 && tile(u - 1) >= t_cut && tile(u - 1) < ntiles)
+                    clean_tile<T, C::TILEB>(buf + (2 + ((u - 1) & 1)) * C::TILEB, threadIdx.x & 255);
+                __syncthreads();
+            }
+            if (tile(u + 1) < ntiles) load_k(u + 1);
+            if (tile(u) < ntiles) load_v(u);
+        };
+        auto kt = [&](int u) SDPA_INLINE -> const uint8_t* { return buf + (u & 1) * C::TILEB; };
+        auto vt = [&](int u) SDPA_INLINE -> const uint8_t* { return buf + (2 + ((u - 1) & 1)) * C::TILEB; };
+        const int u_all = (ntiles + NG - 1) / NG;  // iterations of the longest group
+        const int u_end = NG == 1 ? t_end : t_end > grp ? (t_end - grp + NG - 1) / NG : 0;  // this wave's tiles
+        for (;;) {
+            start();
+            if (tile(0) < ntiles) load_k(0);
+            int u = 0;
+            if (u_end > 0) {
+                stage(0);
+                step(odd, off, on, off, false, -1, kt(0), vt(0));
+                step(even, on, on, off, tile(0) >= t_full, 2 * tile(0), kt(0), vt(0));
+                for (u = 1; u < u_end; ++u) {
+                    stage(u);
+                    step(odd, on, on, on, tile(u - 1) >= t_full, 2 * tile(u - 1) + 1, kt(u), vt(u));
+                    step(even, on, on, on, tile(u) >= t_full, 2 * tile(u), kt(u), vt(u));
+                }
+                stage(u);
+                step(odd, on, off, on, tile(u - 1) >= t_full, 2 * tile(u - 1) + 1, kt(u), vt(u));
+                step(even, off, off, on, false, 0, kt(u), vt(u));
+                ++u;
+            }
+            for (; u <= u_all; ++u) stage(u);
+            if (again || t_cut >= ntiles) break;
+            again = __syncthreads_or(!all_finite<ND>(oacc)) != 0;
+            if (!again) break;
+        }
+        if constexpr (NG > 1) {  // the second group's sums, then the first's join them
+            float* const js = reinterpret_cast<float*>(smem) + wave * ND * 16 * 64 + lane;
+            __syncthreads();
+            if (grp == 1) {
+                ml_s[wave][lane] = make_float2(m, l);
+#pragma unroll
+                for (int d = 0; d < ND; ++d)
+#pragma unroll
+                    for (int r = 0; r < 16; ++r) js[(d * 16 + r) * 64] = oacc[d][r];
+            }
+            __syncthreads();
+            if (grp == 1) return;
+            const float2 o = ml_s[wave][lane];
+            const float up = fmaxf(m, o.x);
+            const float f0 = m == -INFINITY ? 0.0f : fast_exp2(m - up), f1 = o.x == -INFINITY ? 0.0f : fast_exp2(o.x - up);
+            m = up;
+            l = l * f0 + o.y * f1;
 #pragma unroll
             for (int d = 0; d < ND; ++d)
 #pragma unroll
-                for (int r = 0; r < 16; ++r) js[(d * 16 + r) * 64] = oacc[d][r];
+                for (int r = 0; r < 16; ++r) oacc[d][r] = oacc[d][r] * f0 + js[(d * 16 + r) * 64] * f1;
         }
-        __syncthreads();
-        if (grp == 1) return;
-        const float2 o = ml_s[wave * 64 + lane];
-        const float up = fmaxf(m, o.x);
-        const float f0 = m == -INFINITY ? 0.0f : fast_exp2(m - up), f1 = o.x == -INFINITY ? 0.0f : fast_exp2(o.x - up);
-        m = up;
-        l = l * f0 + o.y * f1;
+        if (again) {
+            const rsrc_t vr = make_rsrc(static_cast<const T*>(a.v) + s.k0 * a.v_s[1] + hk * a.v_s[0], a.v_ext);
+            add_kept<T, ND>(vr, vrow, t_cut * TN, kend, a.causal ? qi + s.coff : s.nk - 1, hf, oacc);
+        }
+        store_rows<T, ND>(orr, lr, a, qi, ok, hf, oacc, m, l);
+    } else {
+        // Blocks of 32 keys, every fourth this wave's: its j-th lies in half
+        // j & 1 of its K tile, and of its V tile. An even number of them is
+        // taken; what lies past kend keeps nothing.
+        uint8_t* const kt = smem + wave * 2 * C::TILEB;
+        uint8_t* const vt = kt + C::TILEB;
+        const uint32_t kl = lds_address(kt);
+        constexpr int NB = C::NI / 2;  // copies of a block
+        const int blocks = (kend + 31) / 32, mine = wave < blocks ? ((blocks - wave + NG - 1) / NG + 1) & ~1 : 0;
+        auto block = [&](int j) SDPA_INLINE { return j * NG + wave; };
+        auto load_block = [&](desc_t r, uint32_t dst, int j, uint32_t row, auto order) SDPA_INLINE {
+            const int limit = s.nk - 32 * block(j);
 #pragma unroll
-        for (int d = 0; d < ND; ++d)
-#pragma unroll
-            for (int r = 0; r < 16; ++r)
-                oacc[d][r] = oacc[d][r] * f0 + js[(d * 16 + r) * 64] * f1;
+            for (int i = 0; i < NB; ++i) {
+                const int x = i * C::RPI + lane / C::CPR;
+                copy_to_lds(r, dst + (j & 1) * (C::TILEB / 2) + i * 1024,
+                            pred(x < limit, (uint32_t)(32 * block(j) + x) * row + ((lane % C::CPR) ^ order(x)) * 16));
+            }
+        };
+        auto load_k = [&](int j) SDPA_INLINE { load_block(kd, kl, j, krow, [](int x) { return C::fk(x); }); };
+        auto load_v = [&](int j) SDPA_INLINE { load_block(vd, kl + C::TILEB, j, vrow, [](int x) { return C::fv(x); }); };
+        static_assert(C::fk(32) == 0 && C::fv(32) == 0, "the chunk order of both halves of a tile is the same");
+        const int full = first_cut / 32;  // blocks before hold kept keys only
+        // step j: K block j + 1 and V block j - 1 have landed; behind it the
+        // copies of those that take their places leave
+        auto staged = [&](int j) SDPA_INLINE {
+            if (j + 2 < mine) landed<2 * NB>();
+            else if (j < mine) landed<NB>();
+            else landed<0>();
+            if (again && j > 0 && block(j - 1) >= full) {
+                clean_tile<T, C::TILEB / 2, 64>(vt + ((j - 1) & 1) * (C::TILEB / 2), lane);
+                reads_done();
+            }
+        };
+        auto taken = [&](int j) SDPA_INLINE {
+            reads_done();
+            if (j + 3 < mine) load_k(j + 3);
+            if (j >= 0 && j + 1 < mine) load_v(j + 1);
+        };
+        auto edge = [&](int j) SDPA_INLINE { return block(j) >= full; };
+        for (;;) {
+            start();
+            if (mine == 0) break;
+            load_k(0);
+            load_k(1);
+            load_v(0);
+            staged(-1);
+            step(odd, off, on, off, false, -1, kt, vt);
+            taken(-1);
+            staged(0);
+            step(even, on, on, off, edge(0), block(0), kt, vt);
+            taken(0);
+            int j = 1;
+            for (; j + 1 < mine; j += 2) {
+                staged(j);
+                step(odd, on, on, on, edge(j), block(j), kt, vt);
+                taken(j);
+                staged(j + 1);
+                step(even, on, on, on, edge(j + 1), block(j + 1), kt, vt);
+                taken(j + 1);
+            }
+            staged(j);
+            step(odd, on, off, on, edge(j), block(j), kt, vt);
+            taken(j);
+            staged(j + 1);
+            step(even, off, off, on, false, 0, kt, vt);
+            reads_done();
+            if (again || full >= blocks || __builtin_amdgcn_ballot_w64(!all_finite<ND>(oacc)) == 0) break;
+            again = true;
+        }
+        if (again) {
+            const rsrc_t vr = make_rsrc(static_cast<const T*>(a.v) + s.k0 * a.v_s[1] + hk * a.v_s[0], a.v_ext);
+            for (int j = 0; j < mine; ++j)
+                if (edge(j))
+                    add_kept<T, ND>(vr, vrow, 32 * block(j), min(kend, 32 * block(j) + 32), a.causal ? qi + s.coff : s.nk - 1, hf,
+                                    oacc);
+        }
+        join_waves<T, ND>(orr, lr, a, qi, ok, hf, lane, wave, oacc, m, l, reinterpret_cast<float*>(smem), 2 * C::TILEB / 4, ml_s);
     }
-    if (again) {
-        const rsrc_t vr = make_rsrc(static_cast<const T*>(a.v) + s.k0 * a.v_s[1] + hk * a.v_s[0], a.v_ext);
-        add_kept<T, ND>(vr, vrow, t_cut * TN, kend, a.causal ? qi + s.coff : s.nk - 1, hf, oacc);
-    }
-    store_rows<T, ND>(orr, lr, a, qi, ok, hf, oacc, m, l);
 }
 
-template <typename T, int NG>
+template <typename T, int D>
+static void launch_prompt_td(const PackArgs& a, hipStream_t s) {
+    const dim3 grid((uint32_t)a.B * a.Hq * a.n_blk);
+    if constexpr (sizeof(T) == 4) {
+        sdpa_prompt_f32_kernel<D><<<grid, 256, 0, s>>>(a);
+    } else {
+        if constexpr (D < 128)
+            if (a.groups == 4) {
+                sdpa_prompt_kernel<T, D, 4><<<grid, 256, 0, s>>>(a);
+                return;
+            }
+        if (a.groups == 2) sdpa_prompt_kernel<T, D, 2><<<grid, 512, 0, s>>>(a);
+        else sdpa_prompt_kernel<T, D, 1><<<grid, 256, 0, s>>>(a);
+    }
+}
+
+template <typename T>
 static int launch_prompt_t(int D, const PackArgs& a, hipStream_t s) {
-    const dim3 grid((uint32_t)a.B * a.Hq * a.n_blk), block(256 * NG);
-#define SDPA_PROMPT(D)                                                                    \
-    if constexpr (sizeof(T) == 2) sdpa_prompt_kernel<T, D, NG><<<grid, block, 0, s>>>(a); \
-    else sdpa_prompt_f32_kernel<D><<<grid, block, 0, s>>>(a);
     switch (D) {
-        case 32: SDPA_PROMPT(32) break;
-        case 64: SDPA_PROMPT(64) break;
-        case 128: SDPA_PROMPT(128) break;
+        case 32: launch_prompt_td<T, 32>(a, s); break;
+        case 64: launch_prompt_td<T, 64>(a, s); break;
+        case 128: launch_prompt_td<T, 128>(a, s); break;
         default: return (int)hipErrorInvalidValue;
     }
-#undef SDPA_PROMPT
     return (int)hipGetLastError();
 }
 
 int launch_prompt(int dtype, int D, const PackArgs& a, void* stream) {
     hipStream_t s = static_cast<hipStream_t>(stream);
-    if (dtype == DT_F32) return launch_prompt_t<float, 1>(D, a, s);
-    if (dtype == DT_F16) return a.groups == 2 ? launch_prompt_t<_Float16, 2>(D, a, s) : launch_prompt_t<_Float16, 1>(D, a, s);
-    return a.groups == 2 ? launch_prompt_t<__bf16, 2>(D, a, s) : launch_prompt_t<__bf16, 1>(D, a, s);
+    switch (dtype) {
+        case DT_F32: return launch_prompt_t<float>(D, a, s);
+        case DT_F16: return launch_prompt_t<_Float16>(D, a, s);
+        default: return launch_prompt_t<__bf16>(D, a, s);
+    }
 }
 
 // ------------------------------------------------------------------ key weights

@@ -29,7 +29,7 @@ struct PackArgs {
     int o_vec;            // rows of O take aligned 16-byte stores
     int q_mul;            // 1, or the factor -1 or 0 that the queries are taken with
     float scale_log2;     // |scale| * log2(e) (1 when the scale is 0)
-    int groups;           // prompt: wave groups of the 16-bit kernel (1 or 2)
+    int groups;           // prompt: key groups (1, 2 or 4)
     int n_blk;            // blocks per (sequence, head)
     int n_split;          // key weights: query ranges per key block and query head
     int split_rows;       // key weights: queries of a range
@@ -37,8 +37,7 @@ struct PackArgs {
     uint32_t q_ext, k_ext, v_ext, o_ext, l_ext;  // byte extents of one (sequence, head) slice
 };
 
-constexpr int PROMPT_ROWS = 128;     // query rows of one workgroup of the 16-bit prompt kernel
-constexpr int PROMPT_ROWS_F32 = 32;  // and of the float32 kernel
+constexpr int PROMPT_ROWS = 128;  // query rows of a prompt kernel's workgroup of one or two key groups; of four, a quarter
 int launch_prompt(int dtype, int D, const PackArgs& a, void* stream);
 constexpr int KEY_WEIGHT_KEYS = 128;  // keys of one workgroup of the key-weight kernel
 int launch_key_weights(int dtype, int D, const PackArgs& a, void* stream);

@@ -129,15 +129,24 @@ sdpa_status_t check_cu(int64_t n_seqs, const void* cu_q, const void* cu_k, int i
     return SDPA_OK;
 }
 
-// Prompt attention, 16-bit types: two groups of four waves a workgroup, each on every other
-// key tile, where one group a block leaves wave slots empty (512 workgroups of
-// four waves fill two slots of every SIMD) and the chain of tiles is long
-// enough to pay for joining the groups. Measured, one group and two: 4096
-// tokens x 16 heads of 128 (512 blocks) 91 and 86 us, 1024 x 4 and less ragged
-// ones x 8 heads of 64 (320 blocks) 17.3 and 15.9; 2048 x 4 x 16 heads of 64
-// (1024 blocks) 50 and 61, 512 and 300 tokens x 16 heads 13.7 and 14.3.
-int prompt_groups(const sdpa::PackArgs& a) {
+// Prompt attention: key groups (a wave's chain of tiles is shorter by as
+// much), where blocks of 128 rows leave wave slots empty.
+// float32: always four (rows in blocks of 32).
+// 16 bits, four: up to 256 blocks of 128 rows and D below 128. Measured, four
+// groups and two: 1024 + 700 tokens x 8 heads of 64 (128 blocks) 10.7 and 15.3
+// us, 6000 x 4 of 64 (188) 40.9 and 55.9, 2048 and less ragged ones x 4 of 64
+// (256) 24.8 and 24.5, of 32 14.9 and 20.2, 1024 and less ragged ones x 8 of 64
+// (320) 17.3 and 16.2; 1024 x 4 x 16 of 64 (512) 31 and 23. At D = 128 a CU
+// holds one such workgroup: 20.1 and 21.9, 50 and 35 for 128 and 256 blocks.
+// Two: where one group a block leaves slots empty (512 workgroups of four waves
+// fill two slots of every SIMD) and the chain is long enough to pay for the
+// join. Measured, one group and two: 4096 tokens x 16 heads of 128 (512 blocks)
+// 91 and 86 us, the 320 blocks above 18.5 and 16.2; 2048 x 4 x 16 heads of 64
+// (1024 blocks) 50 and 61, 512 + 300 tokens x 16 heads of 128 13.7 and 14.3.
+int prompt_groups(const sdpa::PackArgs& a, int dtype, int64_t D) {
+    if (dtype == SDPA_F32) return 4;
     const int64_t blocks = (int64_t)a.B * a.Hq * cdiv(a.max_q, sdpa::PROMPT_ROWS);
+    if (D < 128 && blocks <= 256) return 4;
     return blocks <= 512 && a.max_k >= 768 ? 2 : 1;
 }
 
@@ -339,8 +348,8 @@ sdpa_status_t sdpa_prompt_fwd(const sdpa_tensor_t* q, const sdpa_tensor_t* k, co
     TRY(pack_extent(out, "out", a.max_q, out->sizes[2], &a.o_ext));
     TRY(pack_extent(lse, "lse", a.max_q, 1, &a.l_ext));
     const int D = (int)q->sizes[2];
-    a.groups = prompt_groups(a);
-    a.n_blk = (int)cdiv(a.max_q, q->dtype == SDPA_F32 ? sdpa::PROMPT_ROWS_F32 : sdpa::PROMPT_ROWS);
+    a.groups = prompt_groups(a, q->dtype, D);
+    a.n_blk = (int)cdiv(a.max_q, a.groups == 4 ? sdpa::PROMPT_ROWS / 4 : sdpa::PROMPT_ROWS);
     TRY(grid_ok({n_seqs, a.Hq, a.n_blk}));
     return launched(sdpa::launch_prompt(q->dtype, D, a, hip_stream));
 }

@@ -67,6 +67,10 @@ PROMPTS = [
     ("f16-d64-blocks", 24, [1, 31, 33, 97, 800], [1, 31, 33, 97, 800], 2, 1, 64, "f16", True, "top_left", None),
     ("bf16-d32-bottom-right", 25, [5, 300, 64], [900, 300, 777], 4, 2, 32, "bf16", True, "bottom_right", None),
     ("f16-d128-noncausal", 26, [33, 129], [800, 95], 2, 1, 128, "f16", False, "top_left", None),
+    ("two-groups-d64", 31, [800], [800], 40, 8, 64, "f16", True, "top_left", None),
+    ("two-groups-d32", 32, [790, 9], [790, 9], 24, 4, 32, "bf16", True, "top_left", None),
+    ("one-group-d64", 33, [300, 70], [300, 70], 48, 6, 64, "bf16", True, "top_left", None),
+    ("one-group-d32", 34, [400], [400], 72, 9, 32, "f16", True, "top_left", None),
     ("chunk-bottom-right", 8, [16, 100, 37], [200, 100, 300], 4, 2, 64, "f16", True, "bottom_right", None),
     ("more-queries-than-keys", 9, [90, 40], [30, 0], 2, 2, 128, "bf16", True, "bottom_right", None),
     ("noncausal", 10, [5, 9, 64], [77, 0, 129], 2, 2, 128, "bf16", False, "top_left", None),
