@@ -69,6 +69,7 @@ __device__ __forceinline__ void landed() {
     __builtin_amdgcn_sched_barrier(0);
 }
 __device__ __forceinline__ void reads_done() {
+    asm volatile("" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
     __builtin_amdgcn_s_waitcnt(0xC07F);
     __builtin_amdgcn_sched_barrier(0);
@@ -816,7 +817,7 @@ int launch_prompt(int dtype, int D, const PackArgs& a, void* stream) {
 // addition each, to D / 16 products: 549 cycles of the vector unit for 32 rows
 // by 64 keys, measured, to 272 of the matrix unit at D = 64), so it runs four
 // waves a SIMD with little state, whose products and exponentials overlap
-// between waves. 2048 + 1531 tokens, 16 heads of 128: 34 us, against 44 with 64
+// between waves. 2048 + 1531 tokens, 16 heads of 128: 33 us with the sums, against 44 with 64
 // keys a wave (two waves a SIMD) and 38 interleaved by hand as the prompt
 // kernel.
 template <typename T, int D>
