@@ -152,13 +152,17 @@ int prompt_groups(const sdpa::PackArgs& a, int dtype, int64_t D) {
 
 // Key weights: ranges of one query head's rows, enough for 2048 workgroups
 // (two rounds of the 1024 resident ones: the triangle of a causal call needs
-// them to balance), none below 256 rows. Measured with 1024, 2048 and 4096
-// workgroups: 2048 + 1531 tokens x 16 heads of 128 38.7, 32.1 and 36.7 us,
-// 8191 tokens x 16 heads of 64 136, 120 and 128 us.
+// them to balance), of 256 rows at least; of fewer, down to 64, only for the
+// first 512 workgroups. Measured with 1024, 2048 and 4096 workgroups:
+// 2048 + 1531 tokens x 16 heads of 128 38.7, 32.1 and 36.7 us, 8191 tokens x 16
+// heads of 64 136, 120 and 128 us; with at least 256, 128 and 64 rows: 1000
+// tokens x 2 heads of 128 13.1, 11.7 and 11.5 (float32: 45, 30 and 26), but
+// 1024 + 700 x 8 heads of 128 14.5, 17.6 and 21.8.
 void plan_key_weights(sdpa::PackArgs* a) {
     a->n_blk = (int)cdiv(a->max_k, sdpa::KEY_WEIGHT_KEYS);
     const int64_t blocks = std::max<int64_t>(1, (int64_t)a->B * a->Hq * a->n_blk);
-    const int64_t want = std::min<int64_t>(cdiv(2048, blocks), std::max<int64_t>(1, a->max_q / 256));
+    const int64_t want = std::max<int64_t>({1, std::min<int64_t>(cdiv(2048, blocks), a->max_q / 256),
+                                            std::min<int64_t>(cdiv(512, blocks), a->max_q / 64)});
     a->split_rows = (int)std::max<int64_t>(64, cdiv(cdiv(a->max_q, want), 64) * 64);
     a->n_split = (int)std::max<int64_t>(1, cdiv(a->max_q, a->split_rows));
 }
